@@ -31,6 +31,8 @@ int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool cfg_valid(const ufp4_quant_cfg_t &c) {
+    if (c.grid == UFP4_GRID_E4M3)   // 8-bit operands: MX scales, no rotation, RTNE
+        return c.scale_fmt == UFP4_SCALE_UE8M0 && c.block == 32 && c.hadamard_n == 0 && c.rounding == UFP4_ROUND_RTNE;
     if (c.grid != UFP4_GRID_E1M2 && c.grid != UFP4_GRID_E2M1 && c.grid != UFP4_GRID_E2M1_MAX2)
         return false;
     if (c.rounding != UFP4_ROUND_RTNE && c.rounding != UFP4_ROUND_SR) return false;
@@ -104,7 +106,8 @@ ufp4_status_t check_qtensor(const ufp4_qtensor_t *q) {
     if (q->kpad != round_up(q->k, kKAlign)) return UFP4_ERR_INVALID_ARG;
     if (q->scale_ld < q->rows || q->scale_ld % kScaleLdAlign != 0) return UFP4_ERR_INVALID_ARG;
     if (q->rows > 0 && q->kpad > 0) {
-        if (q->codes == nullptr || q->scales == nullptr) return UFP4_ERR_INVALID_ARG;
+        if ((q->cfg.grid == UFP4_GRID_E4M3 ? q->elems8 : q->codes) == nullptr || q->scales == nullptr)
+            return UFP4_ERR_INVALID_ARG;
         if (!aligned16(q->codes) || !aligned16(q->scales)) return UFP4_ERR_ALIGNMENT;
     }
     if (q->cfg.scale_fmt == UFP4_SCALE_E4M3_X_FP32 && q->tensor_scale == nullptr)
@@ -113,8 +116,8 @@ ufp4_status_t check_qtensor(const ufp4_qtensor_t *q) {
         if (q->cfg.grid != UFP4_GRID_E1M2) return UFP4_ERR_INVALID_ARG;
         if (!aligned16(q->corr)) return UFP4_ERR_ALIGNMENT;
     }
-    if (q->elems8 != nullptr) {   // E4M3 element plane of an MX (UE8M0) E1M2 operand
-        if (q->cfg.grid != UFP4_GRID_E1M2 || q->cfg.scale_fmt != UFP4_SCALE_UE8M0) return UFP4_ERR_INVALID_ARG;
+    if (q->elems8 != nullptr) {   // E4M3 elements: an 8-bit operand's, or an MX (UE8M0) E1M2 operand's plane
+        if ((q->cfg.grid != UFP4_GRID_E1M2 && q->cfg.grid != UFP4_GRID_E4M3) || q->cfg.scale_fmt != UFP4_SCALE_UE8M0) return UFP4_ERR_INVALID_ARG;
         if (!aligned16(q->elems8)) return UFP4_ERR_ALIGNMENT;
     }
     if (q->sf_atoms != nullptr) {   // factor atoms: byte block scales only
@@ -141,7 +144,13 @@ ufp4_status_t check_pair(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b, bool 
     s = check_qtensor(b);
     if (s != UFP4_OK) return s;
     const ufp4_quant_cfg_t &x = a->cfg, &y = b->cfg;
-    if (x.grid != y.grid || x.block != y.block || x.scale_fmt != y.scale_fmt ||
+    // 8-bit with 4-bit operands: both as E4M3 elements on the FP8 MMA.
+    const bool mixed8 = (x.grid == UFP4_GRID_E4M3 && y.grid == UFP4_GRID_E1M2) ||
+                        (x.grid == UFP4_GRID_E1M2 && y.grid == UFP4_GRID_E4M3);
+    if (mixed8 && ((a->elems8 == nullptr && a->rows > 0 && a->kpad > 0) ||
+                   (b->elems8 == nullptr && b->rows > 0 && b->kpad > 0)))
+        return UFP4_ERR_OPERAND_MISMATCH;
+    if ((x.grid != y.grid && !mixed8) || x.block != y.block || x.scale_fmt != y.scale_fmt ||
         x.hadamard_n != y.hadamard_n)
         return UFP4_ERR_OPERAND_MISMATCH;
     if (x.hadamard_n > 0 && !same_signs(x.rht_sign_mask, y.rht_sign_mask, x.hadamard_n))
@@ -162,11 +171,11 @@ ufp4_status_t encode_operand_maps(const ufp4_qtensor_t *q, int code_rows, int sc
     const CUtensorMapSwizzle swz = row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                    : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
-    CUresult r = encode_tensor_map_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, q->codes,
-                                      static_cast<uint64_t>(q->kpad / 2),
-                                      static_cast<uint64_t>(rows_t),
-                                      static_cast<uint64_t>(q->kpad / 2), row_bytes,
-                                      static_cast<uint32_t>(code_rows), swz);
+    CUresult r = CUDA_SUCCESS;
+    if (q->cfg.grid != UFP4_GRID_E4M3)   // 8-bit operands have no codes (their elements have their own map)
+        r = encode_tensor_map_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, q->codes, static_cast<uint64_t>(q->kpad / 2),
+                                 static_cast<uint64_t>(rows_t), static_cast<uint64_t>(q->kpad / 2), row_bytes,
+                                 static_cast<uint32_t>(code_rows), swz);
     if (r != CUDA_SUCCESS) return UFP4_ERR_CUDA;
     const int nblk_stage = k_stage / q->cfg.block;
     const uint64_t nblk = static_cast<uint64_t>(q->kpad / q->cfg.block);
@@ -186,13 +195,14 @@ ufp4_status_t encode_operand_maps(const ufp4_qtensor_t *q, int code_rows, int sc
 
 ufp4_status_t run_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
                        const ufp4_group_t *groups_dev, int32_t num_groups, float *c, int64_t ldc,
-                       int64_t m, int64_t n, void *stream) {
+                       int64_t m, int64_t n, void *stream, const EpiArgs *epi = nullptr) {
     // Grouped problems pick their own K window of each operand (a_col, b_col,
     // k per group), so only the quantization settings must agree there.
     ufp4_status_t s = check_pair(a, b, groups_dev == nullptr);
     if (s != UFP4_OK) return s;
-    if (c == nullptr && (m > 0 && n > 0)) return UFP4_ERR_INVALID_ARG;
-    if (ldc < n || ldc < 1) return UFP4_ERR_INVALID_ARG;
+    // With an epilogue the output and its checks are the epilogue's (c = NULL).
+    if (epi == nullptr && c == nullptr && (m > 0 && n > 0)) return UFP4_ERR_INVALID_ARG;
+    if (epi == nullptr && (ldc < n || ldc < 1)) return UFP4_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(c) & 3u) != 0) return UFP4_ERR_ALIGNMENT;
     if (groups_dev != nullptr && (reinterpret_cast<uintptr_t>(groups_dev) & 7u))
         return UFP4_ERR_ALIGNMENT;
@@ -213,13 +223,14 @@ ufp4_status_t run_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
         const bool pair_ok = a->cfg.grid != UFP4_GRID_E1M2 || (adjacent_planes(a) && adjacent_planes(b));
         mode = (g_two_level_path.load() == UFP4_GEMM_PATH_NATIVE_FP4 || !pair_ok) ? 3 : 5;
     }
-    // MX operands that carry E4M3 element planes: the block-scaled FP8 MMA
-    // on CTA pairs (mode 6); otherwise the fp32-block-scale kernel.
-    if (a->cfg.scale_fmt == UFP4_SCALE_UE8M0 && a->cfg.grid == UFP4_GRID_E1M2 && a->elems8 != nullptr &&
-        b->elems8 != nullptr)
-        mode = 6;
+    // MX operands that carry E4M3 element planes (8-bit operands always do):
+    // the block-scaled FP8 MMA on CTA pairs (mode 6); otherwise the
+    // fp32-block-scale kernel.
+    if (a->cfg.scale_fmt == UFP4_SCALE_UE8M0 && a->elems8 != nullptr && b->elems8 != nullptr) mode = 6;
     if (groups_dev == nullptr) {
         if (m == 0 || n == 0) return UFP4_OK;
+        if (a->kpad == 0 && epi != nullptr)
+            return launch_epilogue_only(*epi, m, n, sm_count(), st) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
         if (a->kpad == 0) {
             cudaError_t e = cudaMemset2DAsync(c, static_cast<size_t>(ldc) * 4, 0,
                                               static_cast<size_t>(n) * 4, static_cast<size_t>(m), st);
@@ -349,9 +360,38 @@ ufp4_status_t run_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
     args.band = kTileBand;
     // Native kernels store 16-byte pieces when the output allows it.
     args.c_vec = (aligned16(c) && ldc % 4 == 0) ? 1 : 0;
+    if (epi != nullptr) {
+        args.epilogue = 1;
+        args.epi = *epi;
+    }
     cudaError_t e = launch_gemm(args, mode, grid_kind, sm_count(), st);
     return e == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
 }
+
+bool dtype_valid(int32_t d) { return d == UFP4_DTYPE_BF16 || d == UFP4_DTYPE_FP32; }
+
+int elem_bytes(int32_t d) { return d == UFP4_DTYPE_BF16 ? 2 : 4; }
+
+bool elem_aligned(const void *p, int32_t d) {
+    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(elem_bytes(d) - 1)) == 0;
+}
+
+// `q` consecutive elements from a multiple of q of every row can be accessed
+// with accesses of at most 16 bytes.
+bool row_vec(const void *p, int32_t d, int64_t ld, int q) {
+    const uintptr_t bytes = static_cast<uintptr_t>(q * elem_bytes(d) < 16 ? q * elem_bytes(d) : 16);
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && ld % q == 0;
+}
+
+// A plain [rows][ld] matrix of which `cols` columns are used.
+ufp4_status_t check_matrix(const void *p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
+    if (!dtype_valid(dtype)) return UFP4_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return UFP4_OK;
+    if (p == nullptr || ld < cols) return UFP4_ERR_INVALID_ARG;
+    return elem_aligned(p, dtype) ? UFP4_OK : UFP4_ERR_ALIGNMENT;
+}
+
+bool act_valid(int32_t act) { return act >= UFP4_ACT_NONE && act <= UFP4_ACT_SILU; }
 
 ufp4_status_t check_input(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t axis) {
     if (rows < 0 || cols < 0) return UFP4_ERR_INVALID_ARG;
@@ -370,6 +410,7 @@ ufp4_status_t fill_quant_args(const void *x_dev, int64_t rows, int64_t cols, int
                               const float *tensor_amax_dev, const ufp4_qtensor_t *out, QuantArgs *a) {
     ufp4_status_t s = check_qtensor(out);
     if (s != UFP4_OK) return s;
+    if (out->cfg.grid == UFP4_GRID_E4M3) return UFP4_ERR_UNSUPPORTED;   // 4-bit grids only
     const int64_t out_rows = axis == UFP4_ALONG_COLS ? rows : cols;
     const int64_t K = axis == UFP4_ALONG_COLS ? cols : rows;
     if (out->rows != out_rows || out->k != K) return UFP4_ERR_INVALID_ARG;
@@ -475,7 +516,7 @@ ufp4_status_t ufp4_qtensor_layout(int64_t rows, int64_t k, const ufp4_quant_cfg_
     const int64_t elt = cfg->scale_fmt == UFP4_SCALE_FP32 ? 4 : 1;
     if (kpad) *kpad = kp;
     if (scale_ld) *scale_ld = sl;
-    if (codes_bytes) *codes_bytes = static_cast<size_t>(rows * (kp / 2));
+    if (codes_bytes) *codes_bytes = cfg->grid == UFP4_GRID_E4M3 ? 0 : static_cast<size_t>(rows * (kp / 2));
     if (scales_bytes) *scales_bytes = static_cast<size_t>((kp / cfg->block) * sl * elt);
     return UFP4_OK;
 }
@@ -634,6 +675,7 @@ ufp4_status_t ufp4_quant_stats(const void *x_dev, int64_t rows, int64_t cols, in
     if (s != UFP4_OK) return s;
     s = check_qtensor(q);
     if (s != UFP4_OK) return s;
+    if (q->cfg.grid == UFP4_GRID_E4M3) return UFP4_ERR_UNSUPPORTED;   // 4-bit grids only
     if (stats_dev == nullptr) return UFP4_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(stats_dev) & 7u) != 0) return UFP4_ERR_ALIGNMENT;
     const int64_t out_rows = axis == UFP4_ALONG_COLS ? rows : cols;
@@ -707,6 +749,106 @@ ufp4_status_t ufp4_gemm_wgrad(const ufp4_qtensor_t *dytq, const ufp4_qtensor_t *
                               float *dw_dev, int64_t lddw, void *stream) {
     if (dytq == nullptr || xtq == nullptr) return UFP4_ERR_INVALID_ARG;
     return run_gemm(dytq, xtq, nullptr, 0, dw_dev, lddw, dytq->rows, xtq->rows, stream);
+}
+
+ufp4_status_t ufp4_gemm_epilogue(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b, const ufp4_epilogue_t *epi,
+                                 void *out_dev, int64_t ldo, int32_t out_dtype, void *stream) {
+    if (a == nullptr || b == nullptr) return UFP4_ERR_INVALID_ARG;
+    const int64_t m = a->rows, n = b->rows;
+    if (m < 0 || n < 0) return UFP4_ERR_INVALID_ARG;
+    ufp4_status_t s = check_matrix(out_dev, out_dtype, m, n, ldo);
+    if (s != UFP4_OK) return s;
+    EpiArgs e;
+    memset(&e, 0, sizeof(e));
+    e.out = out_dev;
+    e.ld_out = ldo;
+    e.out_bf16 = out_dtype == UFP4_DTYPE_BF16;
+    e.vec_out = row_vec(out_dev, out_dtype, ldo, 4);
+    if (epi != nullptr) {
+        if (!act_valid(epi->act)) return UFP4_ERR_INVALID_ARG;
+        e.act = epi->act;
+        if (epi->bias != nullptr) {
+            s = check_matrix(epi->bias, epi->bias_dtype, 1, n, n);
+            if (s != UFP4_OK) return s;
+            e.bias = epi->bias;
+            e.bias_bf16 = epi->bias_dtype == UFP4_DTYPE_BF16;
+            e.vec_bias = row_vec(epi->bias, epi->bias_dtype, 0, 4);
+        }
+        if (epi->residual != nullptr) {
+            s = check_matrix(epi->residual, epi->residual_dtype, m, n, epi->ld_residual);
+            if (s != UFP4_OK) return s;
+            e.residual = epi->residual;
+            e.ld_res = epi->ld_residual;
+            e.res_bf16 = epi->residual_dtype == UFP4_DTYPE_BF16;
+            e.vec_res = row_vec(epi->residual, epi->residual_dtype, epi->ld_residual, 4);
+        }
+        if (epi->pre != nullptr) {
+            s = check_matrix(epi->pre, epi->pre_dtype, m, n, epi->ld_pre);
+            if (s != UFP4_OK) return s;
+            e.pre = epi->pre;
+            e.ld_pre = epi->ld_pre;
+            e.pre_bf16 = epi->pre_dtype == UFP4_DTYPE_BF16;
+            e.vec_pre = row_vec(epi->pre, epi->pre_dtype, epi->ld_pre, 4);
+        }
+    }
+    return run_gemm(a, b, nullptr, 0, nullptr, 0, m, n, stream, &e);
+}
+
+size_t ufp4_epilogue_backward_workspace(int64_t m, int64_t n) {
+    if (m <= 0 || n <= 0) return 0;
+    return static_cast<size_t>(epilogue_backward_chunks(m, n)) * static_cast<size_t>(n) * sizeof(float);
+}
+
+ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int32_t dout_dtype,
+                                     const void *pre_dev, int64_t ld_pre, int32_t pre_dtype, int32_t act,
+                                     int64_t m, int64_t n, void *dpre_dev, int64_t ld_dpre, int32_t dpre_dtype,
+                                     float *dbias_dev, void *workspace_dev, void *stream) {
+    if (m < 0 || n < 0 || !act_valid(act) || (dpre_dev == nullptr && dbias_dev == nullptr))
+        return UFP4_ERR_INVALID_ARG;
+    if (m > (int64_t(1) << 31) || n > (int64_t(1) << 31)) return UFP4_ERR_UNSUPPORTED;
+    ufp4_status_t s = check_matrix(dout_dev, dout_dtype, m, n, ld_dout);
+    if (s != UFP4_OK) return s;
+    if (act != UFP4_ACT_NONE) {
+        s = check_matrix(pre_dev, pre_dtype, m, n, ld_pre);
+        if (s != UFP4_OK) return s;
+    }
+    if (dpre_dev != nullptr) {
+        s = check_matrix(dpre_dev, dpre_dtype, m, n, ld_dpre);
+        if (s != UFP4_OK) return s;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n == 0) return UFP4_OK;
+    if (dbias_dev != nullptr) {
+        if (!elem_aligned(dbias_dev, UFP4_DTYPE_FP32)) return UFP4_ERR_ALIGNMENT;
+        if (m == 0)
+            return cudaMemsetAsync(dbias_dev, 0, static_cast<size_t>(n) * sizeof(float), st) == cudaSuccess
+                       ? UFP4_OK
+                       : UFP4_ERR_CUDA;
+        if (workspace_dev == nullptr) return UFP4_ERR_INVALID_ARG;
+        if (!aligned16(workspace_dev)) return UFP4_ERR_ALIGNMENT;
+    }
+    if (m == 0) return UFP4_OK;
+    EpiBwdArgs b;
+    memset(&b, 0, sizeof(b));
+    b.dout = dout_dev;
+    b.pre = pre_dev;
+    b.dpre = dpre_dev;
+    b.dbias = dbias_dev;
+    b.partial = static_cast<float *>(workspace_dev);
+    b.m = m;
+    b.n = n;
+    b.ld_dout = ld_dout;
+    b.ld_pre = ld_pre;
+    b.ld_dpre = ld_dpre;
+    b.dout_bf16 = dout_dtype == UFP4_DTYPE_BF16;
+    b.pre_bf16 = pre_dtype == UFP4_DTYPE_BF16;
+    b.dpre_bf16 = dpre_dtype == UFP4_DTYPE_BF16;
+    b.act = act;
+    b.vec = n % 8 == 0 && row_vec(dout_dev, dout_dtype, ld_dout, 8) &&
+            (act == UFP4_ACT_NONE || row_vec(pre_dev, pre_dtype, ld_pre, 8)) &&
+            (dpre_dev == nullptr || row_vec(dpre_dev, dpre_dtype, ld_dpre, 8));
+    b.chunks = epilogue_backward_chunks(m, n);
+    return launch_epilogue_backward(b, st) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
 }
 
 ufp4_status_t ufp4_grouped_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,

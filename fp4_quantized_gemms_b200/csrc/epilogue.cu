@@ -1,0 +1,262 @@
+// epilogue.cu -- the GEMM epilogue's companions: its backward pass, the
+// epilogue of a product without a reduction dimension, and column sums.
+//
+// Forward (in the GEMM kernels): z = (1/n) A B^T + bias, out = act(z) +
+// residual.  Backward, with dout = dL/dout and z as the forward stored it:
+//     dL/dz        = dout * act'(z)       (dpre; feeds the quantizer of DGRAD and WGRAD)
+//     dL/dbias     = sum over rows of dL/dz
+//     dL/dresidual = dout                 (nothing to compute)
+//
+// epilogue_backward_kernel reads dout and z once and writes dpre once; HBM is
+// its bound (6 bytes per element in bf16, about 15 flops).  A block covers 256
+// columns x a chunk of rows: a lane owns eight columns (one 16-byte bf16
+// access), the eight warps take rows in turn and keep the column sums in fp32
+// registers, so the bias gradient costs no second pass over dpre.  The sums
+// of a chunk go to a partial row, and column_sums_kernel adds the partial
+// rows: no atomics, the same bits every time.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ufp4.h"
+#include "ufp4_elem.cuh"
+#include "ufp4_internal.h"
+
+namespace ufp4 {
+
+namespace {
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWarps = kBwdThreads / 32;
+constexpr int kBwdCols = 256;      // columns of a block
+constexpr int kBwdUnroll = 4;      // rows of a warp in flight
+
+// Eight elements of a row as loaded, bf16 or fp32.
+template <bool BF16>
+struct Raw8 {
+    uint4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const uint4 *q = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i)
+                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
+        w[0] = __ldcs(q);
+        if constexpr (!BF16) w[1] = __ldcs(q + 1);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (BF16) {
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = bf16_lo(u[j]);
+                v[2 * j + 1] = bf16_hi(u[j]);
+            }
+        } else {
+            const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(u[j]);
+        }
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, int64_t i, const float (&v)[8]) {
+    if constexpr (BF16) {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+        float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// Sums of a warp row of columns over the block's warps, written to the
+// chunk's partial row.  Column of (lane, j): 8 lane + j, or lane + 32 j.
+template <bool VEC>
+__device__ __forceinline__ void store_partial(const EpiBwdArgs &a, const float (&sum)[8], int64_t col0) {
+    __shared__ float s_sum[kBwdWarps][kBwdCols];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_sum[warp][VEC ? 8 * lane + j : lane + 32 * j] = sum[j];
+    __syncthreads();
+    const int64_t col = col0 + threadIdx.x;
+    if (col < a.n) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kBwdWarps; ++w) t += s_sum[w][threadIdx.x];
+        a.partial[blockIdx.y * a.n + col] = t;
+    }
+}
+
+template <int ACT, bool DOUT_BF16, bool PRE_BF16, bool DPRE_BF16>
+__global__ void __launch_bounds__(kBwdThreads) epilogue_backward_kernel(const __grid_constant__ EpiBwdArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kBwdCols;
+    const int64_t col = col0 + 8 * lane;
+    const bool col_ok = col < a.n;                     // n % 8 == 0: all eight or none
+    const int64_t r_first = blockIdx.y * a.rows_per_chunk + warp;
+    const int64_t r_end = min(a.m, (blockIdx.y + 1) * a.rows_per_chunk);
+    float sum[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    if (col_ok) {
+        for (int64_t r0 = r_first; r0 < r_end; r0 += kBwdWarps * kBwdUnroll) {
+            Raw8<DOUT_BF16> g[kBwdUnroll];
+            Raw8<PRE_BF16> z[kBwdUnroll];
+#pragma unroll
+            for (int u = 0; u < kBwdUnroll; ++u) {
+                const int64_t r = r0 + kBwdWarps * u;
+                if (r < r_end) {
+                    g[u].load(a.dout, r * a.ld_dout + col);
+                    if constexpr (ACT != UFP4_ACT_NONE) z[u].load(a.pre, r * a.ld_pre + col);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBwdUnroll; ++u) {
+                const int64_t r = r0 + kBwdWarps * u;
+                if (r < r_end) {
+                    float d[8], zv[8];
+                    g[u].get(d);
+                    if constexpr (ACT != UFP4_ACT_NONE) {
+                        z[u].get(zv);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[j] *= act_slope<ACT>(zv[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += d[j];
+                    if (a.dpre != nullptr) store8<DPRE_BF16>(a.dpre, r * a.ld_dpre + col, d);
+                }
+            }
+        }
+    }
+    if (a.dbias != nullptr) store_partial<true>(a, sum, col0);
+}
+
+// Any width, row pitch and alignment: one element per access, a warp's 32
+// lanes side by side.
+template <int ACT>
+__global__ void __launch_bounds__(kBwdThreads) epilogue_backward_any_kernel(const __grid_constant__ EpiBwdArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kBwdCols;
+    const int64_t r_first = blockIdx.y * a.rows_per_chunk + warp;
+    const int64_t r_end = min(a.m, (blockIdx.y + 1) * a.rows_per_chunk);
+    float sum[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    for (int64_t r = r_first; r < r_end; r += kBwdWarps) {
+        float d[8], z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t col = col0 + lane + 32 * j;
+            const bool ok = col < a.n;
+            d[j] = ok ? load_elem(a.dout, r * a.ld_dout + col, a.dout_bf16) : 0.0f;
+            if constexpr (ACT != UFP4_ACT_NONE) z[j] = ok ? load_elem(a.pre, r * a.ld_pre + col, a.pre_bf16) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t col = col0 + lane + 32 * j;
+            if constexpr (ACT != UFP4_ACT_NONE) d[j] *= act_slope<ACT>(z[j]);
+            sum[j] += d[j];
+            if (a.dpre != nullptr && col < a.n) store_elem(a.dpre, r * a.ld_dpre + col, a.dpre_bf16, d[j]);
+        }
+    }
+    if (a.dbias != nullptr) store_partial<false>(a, sum, col0);
+}
+
+// out[c] = sum of the partial rows: 32 columns per block, eight warps take
+// every eighth row, then the eight sums in order.
+__global__ void __launch_bounds__(256) column_sums_kernel(const float *partial, int64_t rows, int64_t cols,
+                                                          float *out) {
+    __shared__ float s_sum[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    float t = 0.0f;
+    if (c < cols) {
+#pragma unroll 4
+        for (int64_t r = warp; r < rows; r += 8) t += partial[r * cols + c];
+    }
+    s_sum[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += s_sum[w][lane];
+        out[c] = s;
+    }
+}
+
+__global__ void __launch_bounds__(256) epilogue_only_kernel(const __grid_constant__ EpiArgs e, int64_t m, int64_t n) {
+    for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
+        for (int64_t col = 4 * threadIdx.x; col < n; col += 4 * 256) {
+            const int valid = col + 4 <= n ? 4 : static_cast<int>(n - col);
+            epilogue_quad(e, row, col, valid, make_float4(0.0f, 0.0f, 0.0f, 0.0f), epilogue_bias(e, col, valid),
+                          epilogue_residual(e, row, col, valid));
+        }
+    }
+}
+
+template <int ACT>
+cudaError_t launch_bwd_act(const EpiBwdArgs &a, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>((a.n + kBwdCols - 1) / kBwdCols), static_cast<unsigned>(a.chunks));
+    if (!a.vec) {
+        epilogue_backward_any_kernel<ACT><<<grid, kBwdThreads, 0, stream>>>(a);
+    } else {
+        const int types = (a.dout_bf16 ? 4 : 0) | (a.pre_bf16 ? 2 : 0) | (a.dpre_bf16 ? 1 : 0);
+        switch (types) {
+            case 0: epilogue_backward_kernel<ACT, false, false, false><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 1: epilogue_backward_kernel<ACT, false, false, true><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 2: epilogue_backward_kernel<ACT, false, true, false><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 3: epilogue_backward_kernel<ACT, false, true, true><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 4: epilogue_backward_kernel<ACT, true, false, false><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 5: epilogue_backward_kernel<ACT, true, false, true><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 6: epilogue_backward_kernel<ACT, true, true, false><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            default: epilogue_backward_kernel<ACT, true, true, true><<<grid, kBwdThreads, 0, stream>>>(a); break;
+        }
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Row chunks: about 24 blocks for each of the GPU's 148 SMs over the whole
+// matrix (several waves, so the last one is a small share), at least 32 rows
+// each.  A function of the shape alone: so are the workspace and the order of
+// the sums.
+int64_t epilogue_backward_chunks(int64_t m, int64_t n) {
+    if (m <= 0 || n <= 0) return 1;
+    const int64_t blocks_n = (n + kBwdCols - 1) / kBwdCols;
+    int64_t chunks = int64_t(148) * 24 / blocks_n;
+    const int64_t most = (m + 31) / 32;
+    if (chunks > most) chunks = most;
+    if (chunks < 1) chunks = 1;
+    const int64_t per = ((m + chunks - 1) / chunks + 7) / 8 * 8;
+    return (m + per - 1) / per;
+}
+
+cudaError_t launch_epilogue_backward(const EpiBwdArgs &args, cudaStream_t stream) {
+    EpiBwdArgs a = args;
+    a.rows_per_chunk = ((a.m + a.chunks - 1) / a.chunks + 7) / 8 * 8;
+    if (a.dbias != nullptr && a.chunks == 1) a.partial = a.dbias;   // the only partial row is the result
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (a.act) {
+        case UFP4_ACT_NONE: e = launch_bwd_act<UFP4_ACT_NONE>(a, stream); break;
+        case UFP4_ACT_RELU: e = launch_bwd_act<UFP4_ACT_RELU>(a, stream); break;
+        case UFP4_ACT_GELU: e = launch_bwd_act<UFP4_ACT_GELU>(a, stream); break;
+        case UFP4_ACT_GELU_ERF: e = launch_bwd_act<UFP4_ACT_GELU_ERF>(a, stream); break;
+        case UFP4_ACT_SILU: e = launch_bwd_act<UFP4_ACT_SILU>(a, stream); break;
+    }
+    if (e != cudaSuccess || a.dbias == nullptr || a.chunks == 1) return e;
+    return launch_column_sums(a.partial, a.chunks, a.n, a.dbias, stream);
+}
+
+cudaError_t launch_column_sums(const float *partial, int64_t rows, int64_t cols, float *out, cudaStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>((cols + 31) / 32);
+    column_sums_kernel<<<blocks, 256, 0, stream>>>(partial, rows, cols, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_epilogue_only(const EpiArgs &e, int64_t m, int64_t n, int num_sms, cudaStream_t stream) {
+    const int64_t cap = static_cast<int64_t>(num_sms) * 8;
+    epilogue_only_kernel<<<static_cast<unsigned>(m < cap ? m : cap), 256, 0, stream>>>(e, m, n);
+    return cudaGetLastError();
+}
+
+}  // namespace ufp4

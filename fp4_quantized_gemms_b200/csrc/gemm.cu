@@ -33,8 +33,11 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #define UFP4_PIPELINE_KERNELS 1
 #include "ufp4_device.cuh"
+#include "ufp4_elem.cuh"
 #include "ufp4_internal.h"
 
 namespace ufp4 {
@@ -251,7 +254,7 @@ __device__ __forceinline__ float ue8m0_to_f32(uint32_t e) {
     return __uint_as_float(e ? (e << 23) : 0x00400000u);
 }
 
-template <int GRID, bool UE8>
+template <int GRID, bool UE8, bool EPI>
 __global__ void __launch_bounds__(F32sCfg::kThreads, 1)
     gemm_f32s_kernel(const __grid_constant__ GemmArgs args) {
     using C = F32sCfg;
@@ -538,7 +541,19 @@ __global__ void __launch_bounds__(F32sCfg::kThreads, 1)
             }
             if (!ok) break;
             const int64_t row = tl.m0 + row_in_tile;
-            if (row < tl.g.m) {
+            if constexpr (EPI) {
+                const int64_t col0 = tl.n0 + 64 * cs;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const int64_t col = col0 + 2 * i;
+                    const int valid = col + 4 <= tl.g.n ? 4 : static_cast<int>(tl.g.n - col);
+                    if (row < tl.g.m && valid > 0)
+                        epilogue_quad(args.epi, row, col, valid,
+                                      make_float4(acc[i].x * mult, acc[i].y * mult, acc[i + 1].x * mult,
+                                                  acc[i + 1].y * mult),
+                                      epilogue_bias(args.epi, col, valid), epilogue_residual(args.epi, row, col, valid));
+                }
+            } else if (row < tl.g.m) {
                 const int64_t col0 = tl.n0 + 64 * cs;
                 float *dst = args.c + (tl.g.c_row + row) * args.ldc + tl.g.c_col + col0;
                 const bool vec = (col0 + 64 <= tl.g.n) && ((reinterpret_cast<uintptr_t>(dst) & 15u) == 0);
@@ -685,7 +700,7 @@ __device__ __forceinline__ void transpose4x4(uint32_t w0, uint32_t w1, uint32_t 
     o[3] = prmt(t1, t3, 0x7632u);
 }
 
-template <int GRID, bool CIN>
+template <int GRID, bool CIN, bool EPI>
 __global__ void __launch_bounds__(Fp4Cfg<GRID, CIN>::kThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ GemmArgs args) {
     using C = Fp4Cfg<GRID, CIN>;
@@ -1037,7 +1052,7 @@ __global__ void __launch_bounds__(Fp4Cfg<GRID, CIN>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     v[i] = tl.g.k > 0 ? __fmul_rn(__uint_as_float(r[i]), mult) : 0.0f;
-                if (vec_tile) {
+                if (EPI || vec_tile) {
                     uint8_t *rowp = buf + row_in_tile * 128;
 #pragma unroll
                     for (int ch = 0; ch < 8; ++ch)
@@ -1052,7 +1067,12 @@ __global__ void __launch_bounds__(Fp4Cfg<GRID, CIN>::kThreads, 1)
                             *reinterpret_cast<const float4 *>(buf + rr * 128 + ((c16 ^ (rr & 7)) << 4));
                         const int64_t grow = m0 + rr;
                         const int64_t gcol = col0 + 4 * c16;
-                        if (grow < tl.g.m && gcol < tl.g.n) {
+                        if constexpr (EPI) {
+                            const int valid = gcol + 4 <= tl.g.n ? 4 : static_cast<int>(tl.g.n - gcol);
+                            if (grow < tl.g.m && valid > 0)
+                                epilogue_quad(args.epi, grow, gcol, valid, val, epilogue_bias(args.epi, gcol, valid),
+                                              epilogue_residual(args.epi, grow, gcol, valid));
+                        } else if (grow < tl.g.m && gcol < tl.g.n) {
                             float *dst = args.c + (tl.g.c_row + grow) * args.ldc + tl.g.c_col + gcol;
                             if (gcol + 4 <= tl.g.n) {
                                 __stcs(reinterpret_cast<float4 *>(dst), val);   // streamed: evict first
@@ -1318,7 +1338,45 @@ __device__ __forceinline__ void store_piece(const GemmArgs &args, const Tile &tl
     }
 }
 
-template <int GRID, bool ATOMS, bool LANES>
+// The same piece through the epilogue (EpiArgs): always transposed through the
+// buffer, so that a lane finishes four consecutive columns of a row, the same
+// four of eight rows: the bias is loaded once per piece, and residual, pre and
+// out move in whole 32-byte sectors.  The residual of four rows is loaded
+// ahead of their arithmetic.
+__device__ __forceinline__ void epilogue_piece(const GemmArgs &args, const Tile &tl, uint8_t *buf, int lane,
+                                               int64_t m0, int64_t col0, uint32_t (&r)[32], float mult) {
+    const EpiArgs &e = args.epi;
+    uint8_t *rowp = buf + lane * 128;
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch)
+        *reinterpret_cast<float4 *>(rowp + ((ch ^ (lane & 7)) << 4)) =
+            make_float4(__fmul_rn(__uint_as_float(r[4 * ch]), mult), __fmul_rn(__uint_as_float(r[4 * ch + 1]), mult),
+                        __fmul_rn(__uint_as_float(r[4 * ch + 2]), mult),
+                        __fmul_rn(__uint_as_float(r[4 * ch + 3]), mult));
+    const int c16 = lane & 7;
+    const int64_t gcol = col0 + 4 * c16;
+    const int valid = gcol + 4 <= tl.g.n ? 4 : static_cast<int>(tl.g.n - gcol);   // <= 0: outside
+    const float4 bias = epilogue_bias(e, gcol, valid);
+    __syncwarp();
+#pragma unroll
+    for (int k0 = 0; k0 < 8; k0 += 4) {
+        float4 res[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t grow = m0 + 4 * (k0 + k) + (lane >> 3);
+            res[k] = epilogue_residual(e, grow, gcol, grow < tl.g.m ? valid : 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int rr = 4 * (k0 + k) + (lane >> 3);
+            const float4 val = *reinterpret_cast<const float4 *>(buf + rr * 128 + ((c16 ^ (rr & 7)) << 4));
+            if (m0 + rr < tl.g.m && valid > 0) epilogue_quad(e, m0 + rr, gcol, valid, val, bias, res[k]);
+        }
+    }
+    __syncwarp();                                     // buffer read out before the next piece
+}
+
+template <int GRID, bool ATOMS, bool LANES, bool EPI>
 __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ GemmArgs args) {
     using C = PairCfg<GRID, ATOMS, LANES>;
@@ -1691,7 +1749,10 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
                 for (int c = 0; c < 4; ++c) {
                     const int64_t col0 = tl.n0 + 128 * h + 32 * c;
                     if (col0 >= tl.g.n) break;            // the same for the whole warp
-                    store_piece(args, tl, buf, lane, m0, col0, r[c], mult, zero, vec_tile);
+                    if constexpr (EPI)
+                        epilogue_piece(args, tl, buf, lane, m0, col0, r[c], mult);
+                    else
+                        store_piece(args, tl, buf, lane, m0, col0, r[c], mult, zero, vec_tile);
                 }
             }
         }
@@ -1705,16 +1766,26 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
     }
 }
 
-template <int GRID, bool ATOMS, bool LANES = false>
-cudaError_t launch_pair(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+// Raises a kernel's dynamic shared memory limit, once per device (the
+// attribute belongs to the device's context).
+template <typename F>
+cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <int GRID, bool ATOMS, bool LANES, bool EPI>
+cudaError_t launch_pair_epi(const GemmArgs &args, int num_sms, cudaStream_t stream) {
     using C = PairCfg<GRID, ATOMS, LANES>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<GRID, ATOMS, LANES>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t ce = allow_smem(gemm_pair_kernel<GRID, ATOMS, LANES, EPI>, C::kAlloc, configured);
+    if (ce != cudaSuccess) return ce;
     int units = num_sms / 2;
     if (args.groups == nullptr) {
         const GemmGroup &g = args.single;
@@ -1734,19 +1805,21 @@ cudaError_t launch_pair(const GemmArgs &args, int num_sms, cudaStream_t stream) 
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<GRID, ATOMS, LANES>, args);
+    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<GRID, ATOMS, LANES, EPI>, args);
 }
 
-template <int GRID, bool CIN>
-cudaError_t launch_fp4(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+template <int GRID, bool ATOMS, bool LANES = false>
+cudaError_t launch_pair(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+    return args.epilogue ? launch_pair_epi<GRID, ATOMS, LANES, true>(args, num_sms, stream)
+                         : launch_pair_epi<GRID, ATOMS, LANES, false>(args, num_sms, stream);
+}
+
+template <int GRID, bool CIN, bool EPI>
+cudaError_t launch_fp4_epi(const GemmArgs &args, int num_sms, cudaStream_t stream) {
     using C = Fp4Cfg<GRID, CIN>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_fp4_kernel<GRID, CIN>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t ce = allow_smem(gemm_fp4_kernel<GRID, CIN, EPI>, C::kAlloc, configured);
+    if (ce != cudaSuccess) return ce;
     int units = num_sms;
     if (args.groups == nullptr) {
         const GemmGroup &g = args.single;
@@ -1754,20 +1827,22 @@ cudaError_t launch_fp4(const GemmArgs &args, int num_sms, cudaStream_t stream) {
         if (tiles < units) units = static_cast<int>(tiles);
     }
     if (units <= 0) return cudaSuccess;
-    gemm_fp4_kernel<GRID, CIN><<<units, C::kThreads, C::kAlloc, stream>>>(args);
+    gemm_fp4_kernel<GRID, CIN, EPI><<<units, C::kThreads, C::kAlloc, stream>>>(args);
     return cudaGetLastError();
 }
 
-template <int GRID, bool UE8>
-cudaError_t launch_f32s_fmt(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+template <int GRID, bool CIN>
+cudaError_t launch_fp4(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+    return args.epilogue ? launch_fp4_epi<GRID, CIN, true>(args, num_sms, stream)
+                         : launch_fp4_epi<GRID, CIN, false>(args, num_sms, stream);
+}
+
+template <int GRID, bool UE8, bool EPI>
+cudaError_t launch_f32s_epi(const GemmArgs &args, int num_sms, cudaStream_t stream) {
     using C = F32sCfg;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_f32s_kernel<GRID, UE8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::kAlloc);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t ce = allow_smem(gemm_f32s_kernel<GRID, UE8, EPI>, C::kAlloc, configured);
+    if (ce != cudaSuccess) return ce;
     int units = num_sms;
     if (args.groups == nullptr) {
         const GemmGroup &g = args.single;
@@ -1775,8 +1850,14 @@ cudaError_t launch_f32s_fmt(const GemmArgs &args, int num_sms, cudaStream_t stre
         if (tiles < units) units = static_cast<int>(tiles);
     }
     if (units <= 0) return cudaSuccess;
-    gemm_f32s_kernel<GRID, UE8><<<units, C::kThreads, C::kAlloc, stream>>>(args);
+    gemm_f32s_kernel<GRID, UE8, EPI><<<units, C::kThreads, C::kAlloc, stream>>>(args);
     return cudaGetLastError();
+}
+
+template <int GRID, bool UE8>
+cudaError_t launch_f32s_fmt(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+    return args.epilogue ? launch_f32s_epi<GRID, UE8, true>(args, num_sms, stream)
+                         : launch_f32s_epi<GRID, UE8, false>(args, num_sms, stream);
 }
 
 // fp32 or UE8M0 block scales: the scale decode is a compile-time choice.

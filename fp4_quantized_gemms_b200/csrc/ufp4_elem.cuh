@@ -1,0 +1,154 @@
+// ufp4_elem.cuh -- element access and the activations of the operators that
+// work on plain bf16 / fp32 tensors (GEMM epilogue, norms, router, clipping).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ufp4_internal.h"
+
+namespace ufp4 {
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two fp32 values to bf16, each rounded to nearest even; `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float load_elem(const void *p, int64_t i, bool bf16) {
+    return bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16)
+                : static_cast<const float *>(p)[i];
+}
+
+__device__ __forceinline__ void store_elem(void *p, int64_t i, bool bf16, float v) {
+    if (bf16)
+        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(p)[i] = v;
+}
+
+// Four consecutive elements from index i: one 8- or 16-byte access when `vec`
+// (the address allows it), else element by element; elements at or beyond
+// `valid` are not touched (read as 0).
+__device__ __forceinline__ float4 load_quad(const void *p, int64_t i, bool bf16, bool vec, int valid) {
+    if (vec && valid >= 4) {
+        if (bf16) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+            return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+        }
+        return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    }
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = e < valid ? load_elem(p, i + e, bf16) : 0.0f;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ void store_quad(void *p, int64_t i, bool bf16, bool vec, int valid, float4 v) {
+    if (vec && valid >= 4) {
+        if (bf16)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) =
+                make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = v;
+        return;
+    }
+    const float e4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < valid) store_elem(p, i + e, bf16, e4[e]);
+}
+
+// ---------------------------------------------------------------------------
+// Activations (ufp4_act_t).  exp is the hardware's ex2 through __expf: its
+// relative error (about 2^-22 plus 2^-24 per unit of the argument) scales a
+// term that is small whenever the argument is large, so every value below is
+// within a few 1e-7 of max(|z|, 1).
+
+// GELU in its tanh form, z (1 + tanh u) / 2 = z / (1 + exp(-2u)),
+// u = sqrt(2 / pi) (z + 0.044715 z^3).
+constexpr float kGeluA = 0.79788456080286536f;   // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+        case UFP4_ACT_RELU: return z < 0.0f ? 0.0f : z;          // NaN stays NaN
+        case UFP4_ACT_GELU: {
+            const float u2 = 2.0f * kGeluA * z * (1.0f + kGeluB * z * z);
+            return __fdividef(z, 1.0f + __expf(-u2));
+        }
+        case UFP4_ACT_GELU_ERF: return 0.5f * z * (1.0f + erff(0.70710678118654752f * z));
+        case UFP4_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+        default: return z;
+    }
+}
+
+__device__ __forceinline__ float4 act_quad(float4 z, int act) {
+    if (act == UFP4_ACT_NONE) return z;
+    return make_float4(act_value(z.x, act), act_value(z.y, act), act_value(z.z, act), act_value(z.w, act));
+}
+
+// Derivative of the activation.  The GELUs and SiLU saturate: beyond |z| = 12
+// (GELU) the derivative is 0 or 1 to fp32, and the clamp keeps the products
+// of a vanishing and a growing factor finite.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == UFP4_ACT_RELU) {
+        return z > 0.0f ? 1.0f : 0.0f;
+    } else if constexpr (ACT == UFP4_ACT_GELU) {
+        const float c = fminf(fmaxf(z, -12.0f), 12.0f);
+        const float c2 = c * c;
+        const float u2 = 2.0f * kGeluA * c * (1.0f + kGeluB * c2);
+        const float t = __expf(fminf(-u2, 80.0f));
+        const float sg = __fdividef(1.0f, 1.0f + t);
+        const float d = sg + c * sg * (t * sg) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * c2);
+        return z == z ? d : z;
+    } else if constexpr (ACT == UFP4_ACT_GELU_ERF) {
+        const float c = fminf(fmaxf(z, -12.0f), 12.0f);
+        const float d = 0.5f * (1.0f + erff(0.70710678118654752f * c)) +
+                        c * 0.39894228040143268f * __expf(-0.5f * c * c);
+        return z == z ? d : z;
+    } else if constexpr (ACT == UFP4_ACT_SILU) {
+        const float c = fminf(fmaxf(z, -80.0f), 80.0f);
+        const float t = __expf(-c);
+        const float sg = __fdividef(1.0f, 1.0f + t);
+        const float d = sg + c * sg * (t * sg);
+        return z == z ? d : z;
+    } else {
+        return 1.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The GEMM epilogue: z = product + bias; pre = z; out = act(z) + residual,
+// all in fp32, each stored value rounded once.
+
+__device__ __forceinline__ float4 add_quad(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// Finishes columns col .. col + valid - 1 (valid <= 4) of a row: z without
+// its bias, the bias and the residual already loaded.
+__device__ __forceinline__ void epilogue_quad(const EpiArgs &e, int64_t row, int64_t col, int valid, float4 z,
+                                              float4 bias, float4 res) {
+    z = add_quad(z, bias);
+    if (e.pre != nullptr) store_quad(e.pre, row * e.ld_pre + col, e.pre_bf16, e.vec_pre, valid, z);
+    const float4 v = add_quad(act_quad(z, e.act), res);
+    store_quad(e.out, row * e.ld_out + col, e.out_bf16, e.vec_out, valid, v);
+}
+
+__device__ __forceinline__ float4 epilogue_bias(const EpiArgs &e, int64_t col, int valid) {
+    if (e.bias == nullptr || valid <= 0) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return load_quad(e.bias, col, e.bias_bf16, e.vec_bias, valid);
+}
+
+__device__ __forceinline__ float4 epilogue_residual(const EpiArgs &e, int64_t row, int64_t col, int valid) {
+    if (e.residual == nullptr || valid <= 0) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return load_quad(e.residual, row * e.ld_res + col, e.res_bf16, e.vec_res, valid);
+}
+
+}  // namespace ufp4

@@ -98,6 +98,20 @@ struct GemmGroup {
     int64_t c_row, c_col;
 };
 
+// Epilogue of a dense GEMM: z = product + bias, pre = z, out = act(z) +
+// residual.  Null pointers: that part is absent.  vec_*: four consecutive
+// elements from a multiple of 4 can be accessed at once.
+struct EpiArgs {
+    const void *bias;        // [n]
+    const void *residual;    // [m][ld_res]
+    void *pre;               // [m][ld_pre]
+    void *out;               // [m][ld_out]
+    int64_t ld_res, ld_pre, ld_out;
+    int32_t bias_bf16, res_bf16, pre_bf16, out_bf16;   // else fp32
+    int32_t vec_bias, vec_res, vec_pre, vec_out;
+    int32_t act;             // ufp4_act_t
+};
+
 struct GemmArgs {
     CUtensorMap tm_a_codes, tm_b_codes;   // u8 [rows][kpad/2]
     CUtensorMap tm_a_scales, tm_b_scales; // [nblk][scale_ld], fp32 or u8
@@ -123,6 +137,8 @@ struct GemmArgs {
     int lanes;                            // A carries per-lane factor tiles (E1M2 pair kernel)
     int atoms;                            // both operands carry factor atoms (pair kernels, dense)
     int band;                             // tile order: rows of tiles per band (0: M fastest)
+    int epilogue;                         // dense problems: `epi` replaces the plain fp32 store to c
+    EpiArgs epi;
 };
 
 // Tile columns (B rows) of the native block-scaled FP4 kernels (modes 3, 4).
@@ -151,6 +167,30 @@ constexpr int pair_stage_k(int grid_kind, bool atoms) { return (grid_kind == 1 &
 // mode 3: two-level scales on the native block-scaled FP4 MMA (kind::mxf4nvf4)
 cudaError_t launch_gemm(const GemmArgs &args, int mode, int grid_kind, int num_sms,
                         cudaStream_t stream);
+
+// out = act(bias) + residual: the epilogue of a product without a reduction
+// dimension (k = 0).
+cudaError_t launch_epilogue_only(const EpiArgs &e, int64_t m, int64_t n, int num_sms, cudaStream_t stream);
+
+// Backward of the epilogue: dpre = dout * act'(pre), dbias = column sums of
+// dpre (unrounded).  Row chunks are summed into partial[chunks][n] and then
+// over the chunks, both in a fixed order.
+struct EpiBwdArgs {
+    const void *dout, *pre;
+    void *dpre;              // or nullptr
+    float *dbias;            // or nullptr
+    float *partial;          // [chunks][n] when dbias
+    int64_t m, n, ld_dout, ld_pre, ld_dpre;
+    int32_t dout_bf16, pre_bf16, dpre_bf16;
+    int32_t act, vec;
+    int64_t chunks, rows_per_chunk;
+};
+int64_t epilogue_backward_chunks(int64_t m, int64_t n);
+cudaError_t launch_epilogue_backward(const EpiBwdArgs &a, cudaStream_t stream);
+
+// out[c] = sum over r < rows of partial[r][c], in row order within fixed
+// groups of rows.
+cudaError_t launch_column_sums(const float *partial, int64_t rows, int64_t cols, float *out, cudaStream_t stream);
 
 // Driver entry point for tensor-map encoding (resolved once at run time).
 CUresult encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,

@@ -20,10 +20,12 @@ LIB_PATH = os.path.join(_HERE, "libufp4.so")
 # enums (include/ufp4.h)
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_OPERAND_MISMATCH, ERR_CUDA, \
     ERR_DEVICE_TIMEOUT = range(7)
-GRID_E1M2, GRID_E2M1, GRID_E2M1_MAX2 = 0, 1, 2
+GRID_E1M2, GRID_E2M1, GRID_E2M1_MAX2, GRID_E4M3 = 0, 1, 2, 3
 ROUND_RTNE, ROUND_SR = 0, 1
 SCALE_FP32, SCALE_E4M3_X_FP32, SCALE_UE8M0 = 0, 1, 2
 ALONG_COLS, ALONG_ROWS = 0, 1
+DTYPE_BF16, DTYPE_FP32 = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_ERF, ACT_SILU = range(5)
 DEFAULT_SIGN_MASK = 0x09F1FD9D03F0A9B4
 
 EXPORTED = [
@@ -33,6 +35,7 @@ EXPORTED = [
     "ufp4_get_two_level_gemm_path", "ufp4_rht_quantize_dual", "ufp4_rht_amax_dual",
     "ufp4_quant_stats", "ufp4_qstats_summarize", "ufp4_sqnr_sums", "ufp4_rht_bf16",
     "ufp4_sf_atoms_layout", "ufp4_sf_lanes_layout", "ufp4_test_set_quantize_wait_limit",
+    "ufp4_gemm_epilogue", "ufp4_epilogue_backward", "ufp4_epilogue_backward_workspace",
 ]
 
 
@@ -60,6 +63,12 @@ class QTensorC(ctypes.Structure):
 class GroupC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("m", "n", "k", "a_row", "a_col", "b_row", "b_col", "c_row", "c_col")]
+
+
+class EpilogueC(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("pre", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("ld_pre", ctypes.c_int64), ("bias_dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("pre_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 class QStatsC(ctypes.Structure):
@@ -118,6 +127,13 @@ def lib() -> ctypes.CDLL:
         L.ufp4_grouped_gemm.restype = st
         L.ufp4_grouped_gemm.argtypes = [ctypes.POINTER(QTensorC), ctypes.POINTER(QTensorC), P,
                                         i32, P, i64, P]
+        L.ufp4_gemm_epilogue.restype = st
+        L.ufp4_gemm_epilogue.argtypes = [ctypes.POINTER(QTensorC), ctypes.POINTER(QTensorC),
+                                         ctypes.POINTER(EpilogueC), P, i64, i32, P]
+        L.ufp4_epilogue_backward_workspace.restype = ctypes.c_size_t
+        L.ufp4_epilogue_backward_workspace.argtypes = [i64, i64]
+        L.ufp4_epilogue_backward.restype = st
+        L.ufp4_epilogue_backward.argtypes = [P, i64, i32, P, i64, i32, i32, i64, i64, P, i64, i32, P, P, P]
         L.ufp4_check_device_status.restype = st
         L.ufp4_check_device_status.argtypes = []
         L.ufp4_sf_atoms_layout.restype = st
@@ -187,7 +203,7 @@ def layout(rows: int, k: int, cfg: QuantConfig):
 @dataclass
 class QTensor:
     """A quantized operand: K-major packed codes + block-major scales."""
-    codes: torch.Tensor          # uint8 [rows, kpad/2]
+    codes: torch.Tensor | None   # uint8 [rows, kpad/2] (None for 8-bit operands, GRID_E4M3)
     scales: torch.Tensor         # float32 or uint8 [kpad/block, scale_ld]
     tensor_scale: torch.Tensor | None   # float32 [1] (two-level only)
     rows: int
@@ -202,7 +218,7 @@ class QTensor:
                                           # factor tiles of a first GEMM operand (E1M2, E4M3 factors)
 
     def c(self) -> QTensorC:
-        return QTensorC(self.codes.data_ptr(), self.scales.data_ptr(),
+        return QTensorC(self.codes.data_ptr() if self.codes is not None else None, self.scales.data_ptr(),
                         self.tensor_scale.data_ptr() if self.tensor_scale is not None else None,
                         self.rows, self.k, self.kpad, self.scale_ld, self.cfg.c(),
                         self.corr.data_ptr() if self.corr is not None else None,
@@ -218,7 +234,7 @@ def wants_corr(cfg: QuantConfig) -> bool:
 
 def wants_elems8(cfg: QuantConfig) -> bool:
     """Operands the block-scaled FP8 GEMM reads as E4M3 elements (MX path)."""
-    return cfg.grid == GRID_E1M2 and cfg.scale_fmt == SCALE_UE8M0
+    return cfg.grid in (GRID_E1M2, GRID_E4M3) and cfg.scale_fmt == SCALE_UE8M0
 
 
 def wants_atoms(cfg: QuantConfig) -> bool:
@@ -265,8 +281,10 @@ def empty_qtensor(rows: int, k: int, cfg: QuantConfig, device="cuda",
         with_corr = wants_corr(cfg)
     # codes and the correction plane in one allocation ([2][rows][kpad/2]):
     # the GEMM then fetches both planes of a tile with one copy
-    planes = torch.empty((2 if with_corr else 1, rows, kpad // 2), dtype=torch.uint8, device=device)
-    codes = planes[0]
+    planes = codes = None
+    if cfg.grid != GRID_E4M3:       # 8-bit operands have elements instead
+        planes = torch.empty((2 if with_corr else 1, rows, kpad // 2), dtype=torch.uint8, device=device)
+        codes = planes[0]
     if cfg.scale_fmt == SCALE_FP32:
         scales = torch.empty((nblk, sld), dtype=torch.float32, device=device)
         ts = None
@@ -440,9 +458,9 @@ def sqnr_sums(ref: torch.Tensor, test: torch.Tensor, out: torch.Tensor | None = 
 
 
 def _gemm(name: str, a: QTensor, b: QTensor, out: torch.Tensor | None) -> torch.Tensor:
-    _require_cuda(a.codes, b.codes)
+    _require_cuda(a.scales, b.scales)
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=torch.float32, device=a.codes.device)
+        out = torch.empty((a.rows, b.rows), dtype=torch.float32, device=a.scales.device)
     ac, bc = a.c(), b.c()
     _check(getattr(lib(), name)(ctypes.byref(ac), ctypes.byref(bc), ctypes.c_void_p(out.data_ptr()),
                                 out.stride(0), _stream_ptr(out.device)), name)
@@ -466,7 +484,7 @@ def gemm_wgrad(dytq: QTensor, xtq: QTensor, out=None) -> torch.Tensor:
 
 def grouped_gemm(a: QTensor, b: QTensor, groups: torch.Tensor, out: torch.Tensor) -> torch.Tensor:
     """groups: int64 CUDA tensor [G, 9] rows (m, n, k, a_row, a_col, b_row, b_col, c_row, c_col)."""
-    _require_cuda(a.codes, b.codes, groups, out)
+    _require_cuda(a.scales, b.scales, groups, out)
     assert groups.dtype == torch.int64 and groups.dim() == 2 and groups.shape[1] == 9
     groups = groups.contiguous()
     ac, bc = a.c(), b.c()
@@ -475,6 +493,112 @@ def grouped_gemm(a: QTensor, b: QTensor, groups: torch.Tensor, out: torch.Tensor
                                    ctypes.c_void_p(out.data_ptr()), out.stride(0),
                                    _stream_ptr(out.device)), "ufp4_grouped_gemm")
     return out
+
+
+# ------------------------------------------- operators around the products
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: bfloat16 or float32, got {t.dtype}")
+    return d
+
+
+def _pitch(t: torch.Tensor, rows: int, cols: int, name: str) -> int:
+    """Row pitch of a [rows, cols] tensor with contiguous rows."""
+    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols, f"{name}: shape {(rows, cols)}, got {tuple(t.shape)}")
+    _need(cols <= 1 or t.stride(1) == 1, f"{name}: rows have to be contiguous")
+    return t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _vector(t: torch.Tensor, n: int, name: str):
+    _need(t.dim() == 1 and t.shape[0] == n and (n <= 1 or t.stride(0) == 1),
+          f"{name}: a contiguous vector of {n}, got {tuple(t.shape)}")
+
+
+def _same_device(device: torch.device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: one call works on one device")
+
+
+def _call(name: str, device: torch.device, *args):
+    """Calls an entry point with `device` current (the tensors' device need
+    not be) on that device's current stream."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(status, name)
+
+
+def _ptr(t: torch.Tensor | None):
+    return t.data_ptr() if t is not None else None
+
+
+def gemm_epilogue(a: QTensor, b: QTensor, bias: torch.Tensor | None = None, act: int = ACT_NONE,
+                  residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  pre: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """out = act(A B^T + bias) + residual from two quantized operands of any
+    of the three GEMMs.  bias [N], residual and pre [M, N]: bfloat16 or
+    float32.  pre receives A B^T + bias (what epilogue_backward needs).
+    out may be the residual itself; out_dtype applies when out is None."""
+    device = a.scales.device
+    _require_cuda(a.scales, b.scales, bias, residual, out, pre)
+    _same_device(device, b.scales, bias, residual, out, pre)
+    m, n = a.rows, b.rows
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=device)
+    od, ldo = _dtype(out, "out"), _pitch(out, m, n, "out")
+    e = EpilogueC(act=act)
+    if bias is not None:
+        _vector(bias, n, "bias")
+        e.bias, e.bias_dtype = bias.data_ptr(), _dtype(bias, "bias")
+    if residual is not None:
+        e.ld_residual = _pitch(residual, m, n, "residual")
+        e.residual, e.residual_dtype = residual.data_ptr(), _dtype(residual, "residual")
+    if pre is not None:
+        e.ld_pre = _pitch(pre, m, n, "pre")
+        e.pre, e.pre_dtype = pre.data_ptr(), _dtype(pre, "pre")
+    _call("ufp4_gemm_epilogue", device, a.c(), b.c(), e, out.data_ptr(), ldo, od)
+    return out
+
+
+def epilogue_backward(dout: torch.Tensor, pre: torch.Tensor | None, act: int, dpre: torch.Tensor | None = None,
+                      want_dbias: bool = True) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """(dpre, dbias) of gemm_epilogue: dpre = dout * act'(pre) (bfloat16 unless
+    a tensor is given), dbias its column sums (float32, or None).  pre may be
+    None for ACT_NONE."""
+    _require_cuda(dout, pre, dpre)
+    device = dout.device
+    _same_device(device, pre, dpre)
+    _need(dout.dim() == 2, "dout: a matrix")
+    m, n = dout.shape
+    gd, ldg = _dtype(dout, "dout"), _pitch(dout, m, n, "dout")
+    zd, ldz = DTYPE_BF16, 0
+    if pre is not None:
+        zd, ldz = _dtype(pre, "pre"), _pitch(pre, m, n, "pre")
+    else:
+        _need(act == ACT_NONE, "pre: needed for an activation")
+    if dpre is None:
+        dpre = torch.empty((m, n), dtype=torch.bfloat16, device=device)
+    dd, ldd = _dtype(dpre, "dpre"), _pitch(dpre, m, n, "dpre")
+    dbias = work = None
+    if want_dbias:
+        dbias = torch.empty(n, dtype=torch.float32, device=device)
+        work = torch.empty(lib().ufp4_epilogue_backward_workspace(m, n), dtype=torch.uint8, device=device)
+    _call("ufp4_epilogue_backward", device, dout.data_ptr(), ldg, gd, _ptr(pre), ldz, zd, act, m, n,
+          dpre.data_ptr(), ldd, dd, _ptr(dbias), _ptr(work))
+    return dpre, dbias
 
 
 GEMM_PATH_AUTO, GEMM_PATH_NATIVE_FP4, GEMM_PATH_NATIVE_FP4_PAIR256 = 0, 3, 5

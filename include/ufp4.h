@@ -23,6 +23,9 @@
  *   5. ufp4_quant_stats / ufp4_qstats_summarize / ufp4_sqnr_sums: the
  *      quantization diagnostics of [PL] §5 and Appendix A (SQNR, level error,
  *      code occupancy, underflow).
+ *   6. What a training step runs around those products: ufp4_gemm_epilogue
+ *      (bias, activation and residual in the GEMM's epilogue) and its
+ *      backward pass.  No counterpart on the pages.
  *
  * Conventions shared by every call:
  *   - All pointers named *_dev, and every pointer inside ufp4_qtensor_t, are
@@ -71,6 +74,13 @@
  *             non-NULL; when both GEMM operands carry one, the GEMM runs on the
  *             block-scaled FP8 MMA with the UE8M0 factors applied in the MMA
  *             (else on the fp32-scale kernel).  Must be NULL otherwise.
+ *             8-bit operands (UFP4_GRID_E4M3; not a format of the method) are
+ *             this plane alone: any E4M3 values, UE8M0 scales of 32-element
+ *             blocks (X = the smallest integer with amax <= 448 * 2^X), no RHT
+ *             (hadamard_n = 0), codes NULL.  The GEMMs multiply them with each
+ *             other or with E1M2 operands with UE8M0 scales, hadamard_n = 0
+ *             and an elems8 plane (8-bit activations, 4-bit weights).  The
+ *             quantizer and the diagnostics do not take them (UNSUPPORTED).
  *   sf_atoms  optional, byte block scales only (E4M3 x fp32 or UE8M0): the
  *             same factors again, in the layout the block-scaled tensor-core
  *             MMA reads its scale factors from (a copy per 32-lane quarter of
@@ -129,11 +139,12 @@ typedef enum {
  * scales map the block maximum to 2.0 and only the E2M1 magnitudes
  * {0, 0.5, 1, 1.5, 2} (codes 0..4) are used; its codes are E2M1 codes, so its
  * operands run on the E2M1 GEMM kernels.  Operands of one GEMM must share a
- * grid (else UFP4_ERR_OPERAND_MISMATCH). */
+ * grid (else UFP4_ERR_OPERAND_MISMATCH), but for E4M3 with E1M2. */
 typedef enum {
     UFP4_GRID_E1M2 = 0,
     UFP4_GRID_E2M1 = 1,
-    UFP4_GRID_E2M1_MAX2 = 2
+    UFP4_GRID_E2M1_MAX2 = 2,
+    UFP4_GRID_E4M3 = 3       /* 8-bit operands, see elems8 above */
 } ufp4_grid_t;
 /* Rounding rules, [PL] §2 "Rounding rules": RTNE for X and W, SR on dY. */
 typedef enum { UFP4_ROUND_RTNE = 0, UFP4_ROUND_SR = 1 } ufp4_round_t;
@@ -193,6 +204,39 @@ typedef struct {
     int64_t b_row, b_col;
     int64_t c_row, c_col;
 } ufp4_group_t;
+
+/* Element types of the plain tensors of the operators around the GEMMs. */
+typedef enum { UFP4_DTYPE_BF16 = 0, UFP4_DTYPE_FP32 = 1 } ufp4_dtype_t;
+
+/* Activations of the GEMM epilogue:
+ *   UFP4_ACT_GELU      z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ *   UFP4_ACT_GELU_ERF  z (1 + erf(z / sqrt 2)) / 2
+ *   UFP4_ACT_SILU      z / (1 + exp(-z)) */
+typedef enum {
+    UFP4_ACT_NONE = 0,
+    UFP4_ACT_RELU = 1,
+    UFP4_ACT_GELU = 2,
+    UFP4_ACT_GELU_ERF = 3,
+    UFP4_ACT_SILU = 4
+} ufp4_act_t;
+
+/* What a GEMM's epilogue does to the product P[M][N]:
+ *   z = P + bias;  pre = z;  out = act(z) + residual
+ * in fp32, each stored value rounded once.  A NULL pointer leaves that part
+ * out.  Pointers are device pointers, element-aligned (rows that are aligned
+ * to four elements get vector accesses).  residual may be out itself (the
+ * same pointer, type and row pitch); otherwise the tensors may not overlap. */
+typedef struct {
+    const void *bias;         /* [N] or NULL                                   */
+    const void *residual;     /* [M][ld_residual] or NULL                      */
+    void *pre;                /* [M][ld_pre] or NULL: z, for the backward pass */
+    int64_t ld_residual;
+    int64_t ld_pre;
+    int32_t bias_dtype;       /* ufp4_dtype_t                                  */
+    int32_t residual_dtype;   /* ufp4_dtype_t                                  */
+    int32_t pre_dtype;        /* ufp4_dtype_t                                  */
+    int32_t act;              /* ufp4_act_t                                    */
+} ufp4_epilogue_t;
 
 /* Default RHT sign mask: bits of splitmix64(0x5EED), any fixed choice works
  * as long as both operands of a GEMM use the same one. */
@@ -338,6 +382,31 @@ ufp4_status_t ufp4_gemm_wgrad(const ufp4_qtensor_t *dytq, const ufp4_qtensor_t *
 ufp4_status_t ufp4_grouped_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
                                 const ufp4_group_t *groups_dev, int32_t num_groups,
                                 float *c_dev, int64_t ldc, void *stream);
+
+/* Block-scaled product with a fused epilogue:
+ *   z = (1/n) A B^T + bias;  out = act(z) + residual   (ufp4_epilogue_t)
+ * a, b: operands of any of the three GEMMs (FPROP: X and W ALONG_COLS, and so
+ * on), of any scale format; out_dev [a->rows][ldo] of out_dtype.  epi may be
+ * NULL (a plain product in out_dtype).  k = 0 gives act(bias) + residual.
+ * Errors: INVALID_ARG, ALIGNMENT, OPERAND_MISMATCH, UNSUPPORTED, CUDA. */
+ufp4_status_t ufp4_gemm_epilogue(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b, const ufp4_epilogue_t *epi,
+                                 void *out_dev, int64_t ldo, int32_t out_dtype, void *stream);
+
+/* Backward of that epilogue over an [m][n] output:
+ *   dpre = dout * act'(pre)          (dL/dz, the gradient of the product)
+ *   dbias[j] = sum_i dout[i][j] * act'(pre[i][j])   (fp32, of the unrounded terms)
+ * dL/dresidual is dout itself.  pre is z as ufp4_gemm_epilogue stored it (may
+ * be NULL for UFP4_ACT_NONE); relu'(0) = 0.  dpre_dev or dbias_dev may be NULL
+ * (not both).  dpre may be dout itself (same pointer, type and pitch).
+ * dbias needs workspace_dev of ufp4_epilogue_backward_workspace(m, n) bytes
+ * (16-byte aligned), used during the call only; calls that may run at the same
+ * time need one each.  The sums are added in a fixed order: the same bits on
+ * every call.  Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+size_t ufp4_epilogue_backward_workspace(int64_t m, int64_t n);
+ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int32_t dout_dtype,
+                                     const void *pre_dev, int64_t ld_pre, int32_t pre_dtype, int32_t act,
+                                     int64_t m, int64_t n, void *dpre_dev, int64_t ld_dpre, int32_t dpre_dtype,
+                                     float *dbias_dev, void *workspace_dev, void *stream);
 
 /* Kernel family for GEMMs whose operands carry two-level (E4M3 x fp32)
  * scales.  Both families run the block-scaled FP4 MMA (kind::mxf4nvf4, UE4M3

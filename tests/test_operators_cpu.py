@@ -1,0 +1,135 @@
+"""Refusals of the operators around the GEMMs: every bad argument is rejected
+on the host, before any CUDA call (no GPU needed)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+from fp4_quantized_gemms_b200 import build as ufp4_build
+from fp4_quantized_gemms_b200 import ufp4
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, BAD, UNSUP, ALIGN, MISMATCH = (ufp4.OK, ufp4.ERR_INVALID_ARG, ufp4.ERR_UNSUPPORTED, ufp4.ERR_ALIGNMENT,
+                                   ufp4.ERR_OPERAND_MISMATCH)
+P = 64 * 1024           # a made-up, well aligned device address
+
+
+@pytest.fixture(scope="module")
+def L():
+    ufp4_build.build()
+    return ufp4.lib()
+
+
+def _layout_of(tmp_path, struct, fields):
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "ufp4.h"\nint main(void) {\n'
+                   f'printf("%zu", sizeof({struct}));\n'
+                   + "".join(f'printf(" %zu", offsetof({struct}, {f}));\n' for f in fields) + "return 0; }\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    return list(map(int, subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()))
+
+
+@pytest.mark.parametrize("struct,mirror", [("ufp4_epilogue_t", "EpilogueC")])
+def test_struct_layouts(tmp_path, struct, mirror):
+    c = getattr(ufp4, mirror)
+    names = [f[0] for f in c._fields_]
+    assert _layout_of(tmp_path, struct, names) == [ctypes.sizeof(c)] + [getattr(c, n).offset for n in names]
+
+
+def _q(rows=128, k=256, elems8=None, **kw):
+    cfg = ufp4.QuantConfig(**kw).c()
+    kp = (k + 63) // 64 * 64
+    codes = None if kw.get("grid") == ufp4.GRID_E4M3 else P
+    return ufp4.QTensorC(codes, 2 * P, 3 * P if kw.get("scale_fmt") == 1 else None, rows, k, kp,
+                         (rows + 63) // 64 * 64, cfg, None, elems8)
+
+
+MX = dict(scale_fmt=ufp4.SCALE_UE8M0, block=32, hadamard_n=0)
+E8 = dict(grid=ufp4.GRID_E4M3, **MX)
+
+
+def test_eight_bit_operands(L):
+    def layout(**kw):
+        c = ufp4.QuantConfig(**kw).c()
+        cb, sb = ctypes.c_size_t(), ctypes.c_size_t()
+        s = L.ufp4_qtensor_layout(100, 130, ctypes.byref(c), None, None, ctypes.byref(cb), ctypes.byref(sb))
+        return s, cb.value, sb.value
+
+    assert layout(**E8) == (OK, 0, 6 * 128)
+    for bad in (dict(scale_fmt=ufp4.SCALE_FP32), dict(block=16), dict(hadamard_n=16), dict(rounding=1)):
+        assert layout(**{**E8, **bad})[0] == BAD
+    q8, q4 = _q(elems8=4 * P, **E8), _q(elems8=5 * P, grid=0, **MX)
+
+    def gemm(a, b, ldc=64):           # ldc < N: a pair that is accepted gets as far as that check
+        return L.ufp4_gemm_fprop(a, b, P, ldc, None)
+
+    assert gemm(q8, q8) == BAD and gemm(q8, q4) == BAD and gemm(q4, q8) == BAD
+    assert gemm(q8, _q(grid=0, **MX)) == MISMATCH                      # no element plane
+    assert gemm(q8, _q(elems8=5 * P, grid=0, scale_fmt=2, block=32, hadamard_n=16)) == MISMATCH
+    assert gemm(q8, _q(grid=1, **MX)) == MISMATCH
+    assert gemm(_q(**E8), q8) == BAD                                   # no elements
+    assert gemm(_q(elems8=4 * P + 8, **E8), q8) == ALIGN
+    x = ctypes.c_void_p(P)
+    assert L.ufp4_rht_quantize(x, 128, 256, 256, 0, None, q8, None) == UNSUP
+    assert L.ufp4_quant_stats(x, 128, 256, 256, 0, q8, P, None) == UNSUP
+
+
+def test_gemm_epilogue(L):
+    a, b = _q(rows=128), _q(rows=64)
+
+    def call(out=P, ldo=64, dt=0, a=a, b=b, **kw):
+        return L.ufp4_gemm_epilogue(a, b, ufp4.EpilogueC(**kw), out, ldo, dt, None)
+
+    assert call(out=None) == BAD and call(ldo=63) == BAD and call(dt=2) == BAD and call(dt=-1) == BAD
+    assert call(out=P + 1) == ALIGN and call(out=P + 2, dt=1) == ALIGN
+    assert call(act=5) == BAD and call(act=-1) == BAD
+    assert call(bias=P, bias_dtype=3) == BAD and call(bias=P + 1) == ALIGN and call(bias=P + 2, bias_dtype=1) == ALIGN
+    assert call(residual=P, ld_residual=63) == BAD and call(residual=P, ld_residual=0) == BAD
+    assert call(residual=P, ld_residual=64, residual_dtype=2) == BAD
+    assert call(residual=P + 1, ld_residual=64) == ALIGN
+    assert call(pre=P, ld_pre=63) == BAD and call(pre=P, ld_pre=64, pre_dtype=9) == BAD
+    assert call(pre=P + 2, ld_pre=64, pre_dtype=1) == ALIGN
+    assert call(b=_q(rows=64, k=192)) == MISMATCH
+    assert L.ufp4_gemm_epilogue(None, b, None, P, 64, 0, None) == BAD
+    assert L.ufp4_gemm_epilogue(a, None, None, P, 64, 0, None) == BAD
+    assert L.ufp4_gemm_epilogue(_q(rows=0), b, None, None, 64, 0, None) == OK      # nothing to write
+
+
+def test_epilogue_backward(L):
+    def call(dout=P, ldg=64, gd=0, pre=P, ldz=64, zd=0, act=2, m=128, n=64, dpre=2 * P, ldd=64, dd=0, dbias=3 * P,
+             work=4 * P):
+        return L.ufp4_epilogue_backward(dout, ldg, gd, pre, ldz, zd, act, m, n, dpre, ldd, dd, dbias, work, None)
+
+    assert call(dout=None) == BAD and call(ldg=63) == BAD and call(gd=2) == BAD and call(dout=P + 1) == ALIGN
+    assert call(pre=None) == BAD and call(ldz=1) == BAD and call(zd=-1) == BAD and call(pre=P + 2, zd=1) == ALIGN
+    assert call(act=7) == BAD and call(m=-1) == BAD and call(n=-1) == BAD and call(m=1 << 32) == UNSUP
+    assert call(ldd=63) == BAD and call(dd=2) == BAD and call(dpre=2 * P + 1) == ALIGN
+    assert call(dpre=None, dbias=None) == BAD and call(dbias=3 * P + 2) == ALIGN
+    assert call(work=None) == BAD and call(work=4 * P + 8) == ALIGN
+    assert call(n=0) == OK
+    W = L.ufp4_epilogue_backward_workspace
+    assert W(0, 64) == 0 and W(64, 0) == 0 and W(1, 64) == 64 * 4
+    assert W(16384, 28672) % (28672 * 4) == 0
+
+
+def test_binding_refusals():
+    """Wrong shapes, types and host tensors raise before the library is called."""
+    cfg = ufp4.QuantConfig(**E8)
+    t = torch.zeros(4, 8)
+    with pytest.raises(RuntimeError, match="CUDA"):
+        ufp4.epilogue_backward(t, t, ufp4.ACT_RELU)
+    with pytest.raises(RuntimeError, match="CUDA"):
+        ufp4.gemm_epilogue(ufp4.empty_qtensor(4, 64, cfg, device="cpu"), ufp4.empty_qtensor(8, 64, cfg, device="cpu"))
+    q = ufp4.empty_qtensor(4, 64, cfg, device="cpu")
+    assert q.codes is None and q.elems8.shape == (4, 64) and q.sf_atoms.shape == (1, 1, 512) and q.c().codes is None
+    with pytest.raises(ValueError, match="bfloat16 or float32"):
+        ufp4._dtype(t.half(), "x")
+    for bad in (t[:3], t.t(), torch.zeros(4, 16)[:, ::2], torch.zeros(8)):
+        with pytest.raises(ValueError):
+            ufp4._pitch(bad, 4, 8, "x")
+    assert ufp4._pitch(torch.zeros(4, 10)[:, :8], 4, 8, "x") == 10
+    with pytest.raises(ValueError):
+        ufp4._vector(torch.zeros(16)[::2], 8, "x")
