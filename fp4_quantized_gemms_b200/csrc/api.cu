@@ -851,6 +851,137 @@ ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int3
     return launch_epilogue_backward(b, st) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
 }
 
+ufp4_status_t ufp4_rmsnorm(const void *x_dev, int64_t ld_x, int32_t x_dtype, const void *residual_dev,
+                           int64_t ld_residual, int32_t stream_dtype, const void *weight_dev, int32_t weight_dtype,
+                           float eps, int64_t rows, int64_t cols, void *h_dev, int64_t ld_h, void *y_dev,
+                           int64_t ld_y, const ufp4_qtensor_t *q, float *rstd_dev, void *stream) {
+    if (rows < 0 || cols < 0 || !(eps >= 0.0f)) return UFP4_ERR_INVALID_ARG;
+    if ((y_dev == nullptr) == (q == nullptr) && rows > 0 && cols > 0) return UFP4_ERR_INVALID_ARG;
+    if (cols > kNormMaxCols || rows > (int64_t(1) << 31) - 4) return UFP4_ERR_UNSUPPORTED;
+    ufp4_status_t s = check_matrix(x_dev, x_dtype, rows, cols, ld_x);
+    if (s != UFP4_OK) return s;
+    if (!dtype_valid(stream_dtype)) return UFP4_ERR_INVALID_ARG;
+    s = check_matrix(weight_dev, weight_dtype, 1, cols, cols);
+    if (s != UFP4_OK) return s;
+    if (residual_dev != nullptr) {
+        s = check_matrix(residual_dev, stream_dtype, rows, cols, ld_residual);
+        if (s != UFP4_OK) return s;
+        s = check_matrix(h_dev, stream_dtype, rows, cols, ld_h);
+        if (s != UFP4_OK) return s;
+    } else if (h_dev != nullptr || stream_dtype != x_dtype) {
+        return UFP4_ERR_INVALID_ARG;
+    }
+    if (y_dev != nullptr) {
+        s = check_matrix(y_dev, UFP4_DTYPE_BF16, rows, cols, ld_y);
+        if (s != UFP4_OK) return s;
+    }
+    if (q != nullptr) {
+        s = check_qtensor(q);
+        if (s != UFP4_OK) return s;
+        if (q->cfg.grid != UFP4_GRID_E4M3) return UFP4_ERR_UNSUPPORTED;   // 4-bit operands come from the quantizer
+        if (q->rows != rows || q->k != cols) return UFP4_ERR_INVALID_ARG;
+    }
+    if (rstd_dev != nullptr && !elem_aligned(rstd_dev, UFP4_DTYPE_FP32)) return UFP4_ERR_ALIGNMENT;
+    if (rows == 0 || cols == 0) return UFP4_OK;
+    NormArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = x_dev;
+    a.residual = residual_dev;
+    a.weight = weight_dev;
+    a.h = h_dev;
+    a.y = y_dev;
+    a.rstd = rstd_dev;
+    a.rows = rows;
+    a.cols = cols;
+    a.kpad = cols;
+    a.ld_x = ld_x;
+    a.ld_res = ld_residual;
+    a.ld_h = ld_h;
+    a.ld_y = ld_y;
+    if (q != nullptr) {
+        a.elems8 = static_cast<uint8_t *>(q->elems8);
+        a.scales = static_cast<uint8_t *>(q->scales);
+        a.sf_atoms = static_cast<uint8_t *>(q->sf_atoms);
+        a.kpad = q->kpad;
+        a.scale_ld = q->scale_ld;
+        a.atoms_k = atoms_k_of(q->kpad, q->cfg);
+    }
+    a.eps = eps;
+    a.x_bf16 = x_dtype == UFP4_DTYPE_BF16;
+    a.stream_bf16 = stream_dtype == UFP4_DTYPE_BF16;
+    a.weight_bf16 = weight_dtype == UFP4_DTYPE_BF16;
+    a.vec = cols % 8 == 0 && row_vec(x_dev, x_dtype, ld_x, 8) &&
+            (residual_dev == nullptr || (row_vec(residual_dev, stream_dtype, ld_residual, 8) &&
+                                         row_vec(h_dev, stream_dtype, ld_h, 8))) &&
+            (y_dev == nullptr || row_vec(y_dev, UFP4_DTYPE_BF16, ld_y, 8));
+    a.vec_weight = cols % 8 == 0 && row_vec(weight_dev, weight_dtype, 0, 8);
+    return launch_rmsnorm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
+}
+
+size_t ufp4_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0) return 0;
+    return static_cast<size_t>(rmsnorm_backward_slots(rows, cols)) * static_cast<size_t>(cols) * sizeof(float);
+}
+
+ufp4_status_t ufp4_rmsnorm_backward(const void *dy_dev, int64_t ld_dy, int32_t dy_dtype, const void *h_dev,
+                                    int64_t ld_h, int32_t stream_dtype, const void *weight_dev,
+                                    int32_t weight_dtype, const float *rstd_dev, const void *dh_dev, int64_t ld_dh,
+                                    int64_t rows, int64_t cols, void *dx_dev, int64_t ld_dx, int32_t dx_dtype,
+                                    float *dweight_dev, void *workspace_dev, void *stream) {
+    if (rows < 0 || cols < 0) return UFP4_ERR_INVALID_ARG;
+    if (cols > kNormMaxCols || rows > (int64_t(1) << 31) - 4) return UFP4_ERR_UNSUPPORTED;
+    ufp4_status_t s = check_matrix(dy_dev, dy_dtype, rows, cols, ld_dy);
+    if (s != UFP4_OK) return s;
+    s = check_matrix(h_dev, stream_dtype, rows, cols, ld_h);
+    if (s != UFP4_OK) return s;
+    s = check_matrix(weight_dev, weight_dtype, 1, cols, cols);
+    if (s != UFP4_OK) return s;
+    if (dh_dev != nullptr) {
+        s = check_matrix(dh_dev, stream_dtype, rows, cols, ld_dh);
+        if (s != UFP4_OK) return s;
+    }
+    s = check_matrix(dx_dev, dx_dtype, rows, cols, ld_dx);
+    if (s != UFP4_OK) return s;
+    if (cols == 0) return UFP4_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dweight_dev != nullptr) {
+        if (!elem_aligned(dweight_dev, UFP4_DTYPE_FP32)) return UFP4_ERR_ALIGNMENT;
+        if (rows == 0)
+            return cudaMemsetAsync(dweight_dev, 0, static_cast<size_t>(cols) * sizeof(float), st) == cudaSuccess
+                       ? UFP4_OK
+                       : UFP4_ERR_CUDA;
+        if (workspace_dev == nullptr) return UFP4_ERR_INVALID_ARG;
+        if (!aligned16(workspace_dev)) return UFP4_ERR_ALIGNMENT;
+    }
+    if (rows == 0) return UFP4_OK;
+    if (rstd_dev == nullptr) return UFP4_ERR_INVALID_ARG;
+    if (!elem_aligned(rstd_dev, UFP4_DTYPE_FP32)) return UFP4_ERR_ALIGNMENT;
+    NormBwdArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dy = dy_dev;
+    a.h = h_dev;
+    a.weight = weight_dev;
+    a.dh = dh_dev;
+    a.rstd = rstd_dev;
+    a.dx = dx_dev;
+    a.dweight = dweight_dev;
+    a.partial = static_cast<float *>(workspace_dev);
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_dy = ld_dy;
+    a.ld_h = ld_h;
+    a.ld_dh = ld_dh;
+    a.ld_dx = ld_dx;
+    a.dy_bf16 = dy_dtype == UFP4_DTYPE_BF16;
+    a.stream_bf16 = stream_dtype == UFP4_DTYPE_BF16;
+    a.dx_bf16 = dx_dtype == UFP4_DTYPE_BF16;
+    a.weight_bf16 = weight_dtype == UFP4_DTYPE_BF16;
+    a.vec = cols % 8 == 0 && row_vec(dy_dev, dy_dtype, ld_dy, 8) && row_vec(h_dev, stream_dtype, ld_h, 8) &&
+            (dh_dev == nullptr || row_vec(dh_dev, stream_dtype, ld_dh, 8)) && row_vec(dx_dev, dx_dtype, ld_dx, 8);
+    a.vec_weight = cols % 8 == 0 && row_vec(weight_dev, weight_dtype, 0, 8);
+    return launch_rmsnorm_backward(a, st) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
+}
+
 ufp4_status_t ufp4_grouped_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
                                 const ufp4_group_t *groups_dev, int32_t num_groups, float *c_dev,
                                 int64_t ldc, void *stream) {

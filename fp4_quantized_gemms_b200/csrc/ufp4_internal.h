@@ -192,6 +192,34 @@ cudaError_t launch_epilogue_backward(const EpiBwdArgs &a, cudaStream_t stream);
 // groups of rows.
 cudaError_t launch_column_sums(const float *partial, int64_t rows, int64_t cols, float *out, cudaStream_t stream);
 
+// RMS norm (norm.cu).  vec: cols % 8 == 0 and every matrix allows 16-byte
+// accesses of eight (bf16) or four (fp32) elements.
+constexpr int64_t kNormMaxCols = 32768;   // a row is held in the registers of one block
+struct NormArgs {
+    const void *x, *residual, *weight;    // residual or nullptr
+    void *h;                              // x + residual (with a residual)
+    void *y;                              // bf16 output, or nullptr
+    uint8_t *elems8, *scales, *sf_atoms;  // 8-bit output, or nullptr (atoms optional)
+    float *rstd;                          // [rows] or nullptr
+    int64_t rows, cols, kpad;             // kpad: elements per row of the 8-bit output
+    int64_t ld_x, ld_res, ld_h, ld_y, scale_ld, atoms_k;
+    float eps;
+    int32_t x_bf16, stream_bf16, weight_bf16, vec, vec_weight;
+};
+cudaError_t launch_rmsnorm(const NormArgs &a, cudaStream_t stream);
+
+struct NormBwdArgs {
+    const void *dy, *h, *weight, *dh;     // dh or nullptr
+    const float *rstd;
+    void *dx;
+    float *dweight;                       // or nullptr
+    float *partial;                       // [slots][cols] when dweight
+    int64_t rows, cols, ld_dy, ld_h, ld_dh, ld_dx;
+    int32_t dy_bf16, stream_bf16, dx_bf16, weight_bf16, vec, vec_weight;
+};
+int64_t rmsnorm_backward_slots(int64_t rows, int64_t cols);
+cudaError_t launch_rmsnorm_backward(const NormBwdArgs &a, cudaStream_t stream);
+
 // Driver entry point for tensor-map encoding (resolved once at run time).
 CUresult encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,
                               uint64_t inner, uint64_t outer, uint64_t row_bytes,

@@ -36,6 +36,7 @@ EXPORTED = [
     "ufp4_quant_stats", "ufp4_qstats_summarize", "ufp4_sqnr_sums", "ufp4_rht_bf16",
     "ufp4_sf_atoms_layout", "ufp4_sf_lanes_layout", "ufp4_test_set_quantize_wait_limit",
     "ufp4_gemm_epilogue", "ufp4_epilogue_backward", "ufp4_epilogue_backward_workspace",
+    "ufp4_rmsnorm", "ufp4_rmsnorm_backward", "ufp4_rmsnorm_backward_workspace",
 ]
 
 
@@ -134,6 +135,15 @@ def lib() -> ctypes.CDLL:
         L.ufp4_epilogue_backward_workspace.argtypes = [i64, i64]
         L.ufp4_epilogue_backward.restype = st
         L.ufp4_epilogue_backward.argtypes = [P, i64, i32, P, i64, i32, i32, i64, i64, P, i64, i32, P, P, P]
+        f32 = ctypes.c_float
+        L.ufp4_rmsnorm.restype = st
+        L.ufp4_rmsnorm.argtypes = [P, i64, i32, P, i64, i32, P, i32, f32, i64, i64, P, i64, P, i64,
+                                   ctypes.POINTER(QTensorC), P, P]
+        L.ufp4_rmsnorm_backward_workspace.restype = ctypes.c_size_t
+        L.ufp4_rmsnorm_backward_workspace.argtypes = [i64, i64]
+        L.ufp4_rmsnorm_backward.restype = st
+        L.ufp4_rmsnorm_backward.argtypes = [P, i64, i32, P, i64, i32, P, i32, P, P, i64, i64, i64, P, i64, i32, P,
+                                            P, P]
         L.ufp4_check_device_status.restype = st
         L.ufp4_check_device_status.argtypes = []
         L.ufp4_sf_atoms_layout.restype = st
@@ -599,6 +609,85 @@ def epilogue_backward(dout: torch.Tensor, pre: torch.Tensor | None, act: int, dp
     _call("ufp4_epilogue_backward", device, dout.data_ptr(), ldg, gd, _ptr(pre), ldz, zd, act, m, n,
           dpre.data_ptr(), ldd, dd, _ptr(dbias), _ptr(work))
     return dpre, dbias
+
+
+CFG_8BIT = QuantConfig(grid=GRID_E4M3, hadamard_n=0, block=32, scale_fmt=SCALE_UE8M0)
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+            y: torch.Tensor | None = None, q: QTensor | None = None, h: torch.Tensor | None = None,
+            rstd: torch.Tensor | None = None):
+    """RMS norm of the residual stream: h = x + residual (in the residual's
+    type), y = h * rstd * weight.  Returns (y, q, h, rstd).
+
+    The output is bfloat16 (y, allocated unless given) or, when q is given,
+    an 8-bit GEMM operand (empty_qtensor(rows, cols, CFG_8BIT)).  h is x when
+    there is no residual; h may be the residual itself (or x) to update the
+    stream in place.  rstd [rows] float32 is what rmsnorm_backward needs."""
+    _require_cuda(x, weight, residual, y, h, rstd, q.scales if q is not None else None)
+    device = x.device
+    _same_device(device, weight, residual, y, h, rstd, q.scales if q is not None else None)
+    _need(x.dim() == 2, "x: a matrix")
+    rows, cols = x.shape
+    xd, ldx = _dtype(x, "x"), _pitch(x, rows, cols, "x")
+    _vector(weight, cols, "weight")
+    _need(y is None or q is None, "y or q: one output")
+    ldr = ldh = ldy = 0
+    sd = xd
+    if residual is not None:
+        sd, ldr = _dtype(residual, "residual"), _pitch(residual, rows, cols, "residual")
+        if h is None:
+            h = torch.empty((rows, cols), dtype=residual.dtype, device=device)
+        _need(h.dtype == residual.dtype, "h: the residual's type")
+        ldh = _pitch(h, rows, cols, "h")
+    else:
+        _need(h is None, "h: x itself without a residual")
+    if q is None:
+        if y is None:
+            y = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+        _need(y.dtype == torch.bfloat16, "y: bfloat16")
+        ldy = _pitch(y, rows, cols, "y")
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    _need(rstd.dtype == torch.float32, "rstd: float32")
+    _vector(rstd, rows, "rstd")
+    _call("ufp4_rmsnorm", device, x.data_ptr(), ldx, xd, _ptr(residual), ldr, sd, weight.data_ptr(),
+          _dtype(weight, "weight"), eps, rows, cols, _ptr(h), ldh, _ptr(y), ldy, q.c() if q is not None else None,
+          rstd.data_ptr())
+    return y, q, h if h is not None else x, rstd
+
+
+def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dh: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                     want_dweight: bool = True) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """(dx, dweight) of rmsnorm: dx is the gradient of x and of the residual
+    (the stream's type unless a tensor is given), with dh, the gradient that
+    arrives at h itself, added in; dweight float32 (or None)."""
+    _require_cuda(dy, h, weight, rstd, dh, dx)
+    device = h.device
+    _same_device(device, dy, weight, rstd, dh, dx)
+    _need(h.dim() == 2, "h: a matrix")
+    rows, cols = h.shape
+    sd, ldh = _dtype(h, "h"), _pitch(h, rows, cols, "h")
+    gd, ldg = _dtype(dy, "dy"), _pitch(dy, rows, cols, "dy")
+    _vector(weight, cols, "weight")
+    _vector(rstd, rows, "rstd")
+    _need(rstd.dtype == torch.float32, "rstd: float32")
+    lddh = 0
+    if dh is not None:
+        _need(dh.dtype == h.dtype, "dh: the stream's type")
+        lddh = _pitch(dh, rows, cols, "dh")
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=h.dtype, device=device)
+    dd, lddx = _dtype(dx, "dx"), _pitch(dx, rows, cols, "dx")
+    dweight = work = None
+    if want_dweight:
+        dweight = torch.empty(cols, dtype=torch.float32, device=device)
+        work = torch.empty(lib().ufp4_rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=device)
+    _call("ufp4_rmsnorm_backward", device, dy.data_ptr(), ldg, gd, h.data_ptr(), ldh, sd, weight.data_ptr(),
+          _dtype(weight, "weight"), rstd.data_ptr(), _ptr(dh), lddh, rows, cols, dx.data_ptr(), lddx, dd,
+          _ptr(dweight), _ptr(work))
+    return dx, dweight
 
 
 GEMM_PATH_AUTO, GEMM_PATH_NATIVE_FP4, GEMM_PATH_NATIVE_FP4_PAIR256 = 0, 3, 5

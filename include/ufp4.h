@@ -24,8 +24,9 @@
  *      quantization diagnostics of [PL] §5 and Appendix A (SQNR, level error,
  *      code occupancy, underflow).
  *   6. What a training step runs around those products: ufp4_gemm_epilogue
- *      (bias, activation and residual in the GEMM's epilogue) and its
- *      backward pass.  No counterpart on the pages.
+ *      (bias, activation and residual in the GEMM's epilogue) and
+ *      ufp4_rmsnorm (RMS norm of the residual stream, bf16 or 8-bit operand
+ *      out), each with its backward pass.  No counterpart on the pages.
  *
  * Conventions shared by every call:
  *   - All pointers named *_dev, and every pointer inside ufp4_qtensor_t, are
@@ -76,7 +77,8 @@
  *             (else on the fp32-scale kernel).  Must be NULL otherwise.
  *             8-bit operands (UFP4_GRID_E4M3; not a format of the method) are
  *             this plane alone: any E4M3 values, UE8M0 scales of 32-element
- *             blocks (X = the smallest integer with amax <= 448 * 2^X), no RHT
+ *             blocks (X = the smallest integer with amax <= 448 * 2^X), zeros
+ *             as 0x00, no RHT
  *             (hadamard_n = 0), codes NULL.  The GEMMs multiply them with each
  *             other or with E1M2 operands with UE8M0 scales, hadamard_n = 0
  *             and an elems8 plane (8-bit activations, 4-bit weights).  The
@@ -407,6 +409,46 @@ ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int3
                                      const void *pre_dev, int64_t ld_pre, int32_t pre_dtype, int32_t act,
                                      int64_t m, int64_t n, void *dpre_dev, int64_t ld_dpre, int32_t dpre_dtype,
                                      float *dbias_dev, void *workspace_dev, void *stream);
+
+/* Root-mean-square norm of a residual stream, per row of [rows][cols]:
+ *   h = x + residual     (rounded to stream_dtype and stored; without a residual h is x)
+ *   r = 1 / sqrt(mean(h^2) + eps);  y = h * r * weight
+ *   x_dev         [rows][ld_x] of x_dtype.
+ *   residual_dev  [rows][ld_residual] of stream_dtype, or NULL (then h_dev is
+ *                 NULL too and stream_dtype is x_dtype).
+ *   weight_dev    [cols] of weight_dtype.
+ *   h_dev         [rows][ld_h] of stream_dtype, receives h; may be residual_dev
+ *                 itself, or x_dev itself (same type and pitch).
+ *   y_dev         bf16 [rows][ld_y], or NULL when q is given.
+ *   q             8-bit operand (UFP4_GRID_E4M3; elems8, scales and optionally
+ *                 sf_atoms buffers; rows = rows, k = cols) that receives y, or
+ *                 NULL: exactly one of y_dev and q.  Columns cols .. kpad - 1
+ *                 of its elements are set to 0; scale entries and atom bytes of
+ *                 rows beyond `rows` are left alone.  It goes straight into
+ *                 the GEMMs as their ALONG_COLS operand.
+ *   rstd_dev      fp32 [rows], receives r (for the backward pass), or NULL.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (cols > 32768), CUDA. */
+ufp4_status_t ufp4_rmsnorm(const void *x_dev, int64_t ld_x, int32_t x_dtype, const void *residual_dev,
+                           int64_t ld_residual, int32_t stream_dtype, const void *weight_dev, int32_t weight_dtype,
+                           float eps, int64_t rows, int64_t cols, void *h_dev, int64_t ld_h, void *y_dev,
+                           int64_t ld_y, const ufp4_qtensor_t *q, float *rstd_dev, void *stream);
+
+/* Backward of the norm, with g = dy * weight and xhat = h * r:
+ *   dx = r * (g - xhat * mean(g * xhat)) + dh   (gradient of x and of the residual)
+ *   dweight[j] = sum_i dy[i][j] * xhat[i][j]    (fp32)
+ * h is the stream as the forward stored it (x without a residual), rstd its r,
+ * dh the gradient that arrives at h from its other readers (stream_dtype, or
+ * NULL).  dx_dev of dx_dtype; it may be dh or dy itself (same type and pitch).
+ * dweight_dev may be NULL; it needs workspace_dev of
+ * ufp4_rmsnorm_backward_workspace(rows, cols) bytes (16-byte aligned), used
+ * during the call only; calls that may run at the same time need one each.
+ * The sums are added in a fixed order.  Errors: as ufp4_rmsnorm. */
+size_t ufp4_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+ufp4_status_t ufp4_rmsnorm_backward(const void *dy_dev, int64_t ld_dy, int32_t dy_dtype, const void *h_dev,
+                                    int64_t ld_h, int32_t stream_dtype, const void *weight_dev,
+                                    int32_t weight_dtype, const float *rstd_dev, const void *dh_dev, int64_t ld_dh,
+                                    int64_t rows, int64_t cols, void *dx_dev, int64_t ld_dx, int32_t dx_dtype,
+                                    float *dweight_dev, void *workspace_dev, void *stream);
 
 /* Kernel family for GEMMs whose operands carry two-level (E4M3 x fp32)
  * scales.  Both families run the block-scaled FP4 MMA (kind::mxf4nvf4, UE4M3

@@ -133,3 +133,47 @@ def test_binding_refusals():
     assert ufp4._pitch(torch.zeros(4, 10)[:, :8], 4, 8, "x") == 10
     with pytest.raises(ValueError):
         ufp4._vector(torch.zeros(16)[::2], 8, "x")
+
+
+def test_rmsnorm(L):
+    q = _q(rows=128, k=64, elems8=4 * P, **E8)
+
+    def call(x=P, ldx=64, xd=0, res=2 * P, ldr=64, sd=0, w=3 * P, wd=0, eps=1e-6, rows=128, cols=64, h=5 * P, ldh=64,
+             y=6 * P, ldy=64, q=None, rstd=7 * P):
+        return L.ufp4_rmsnorm(x, ldx, xd, res, ldr, sd, w, wd, eps, rows, cols, h, ldh, y, ldy, q, rstd, None)
+
+    assert call(x=None) == BAD and call(ldx=63) == BAD and call(xd=2) == BAD and call(x=P + 1) == ALIGN
+    assert call(ldr=63) == BAD and call(sd=5) == BAD and call(res=2 * P + 2, sd=1) == ALIGN
+    assert call(w=None) == BAD and call(wd=-1) == BAD and call(w=3 * P + 2, wd=1) == ALIGN
+    assert call(eps=-1.0) == BAD and call(eps=float("nan")) == BAD
+    assert call(rows=-1) == BAD and call(cols=-1) == BAD
+    assert call(cols=32769, ldx=32769, ldr=32769, ldh=32769, ldy=32769) == UNSUP
+    assert call(h=None) == BAD and call(ldh=1) == BAD
+    assert call(res=None) == BAD                          # h without a residual
+    assert call(res=None, h=None, sd=1) == BAD            # a stream type of its own
+    assert call(y=None) == BAD and call(q=q) == BAD       # none, both
+    assert call(ldy=63) == BAD and call(y=6 * P + 1) == ALIGN and call(rstd=7 * P + 2) == ALIGN
+    assert call(y=None, q=_q(rows=127, k=64, elems8=4 * P, **E8)) == BAD
+    assert call(y=None, q=_q(rows=128, k=128, elems8=4 * P, **E8)) == BAD
+    assert call(y=None, q=_q(rows=128, k=64, **E8)) == BAD                     # no elements
+    assert call(y=None, q=_q(rows=128, k=64, elems8=4 * P + 4, **E8)) == ALIGN
+    assert call(y=None, q=_q(rows=128, k=64, elems8=4 * P, grid=0, **MX)) == UNSUP
+    assert call(rows=0) == OK
+
+
+def test_rmsnorm_backward(L):
+    def call(dy=P, ldg=64, gd=0, h=2 * P, ldh=64, sd=0, w=3 * P, wd=0, rstd=4 * P, dh=5 * P, lddh=64, rows=128,
+             cols=64, dx=6 * P, lddx=64, dd=0, dw=7 * P, work=8 * P):
+        return L.ufp4_rmsnorm_backward(dy, ldg, gd, h, ldh, sd, w, wd, rstd, dh, lddh, rows, cols, dx, lddx, dd, dw,
+                                       work, None)
+
+    assert call(dy=None) == BAD and call(ldg=63) == BAD and call(gd=2) == BAD and call(dy=P + 1) == ALIGN
+    assert call(h=None) == BAD and call(ldh=63) == BAD and call(sd=2) == BAD and call(h=2 * P + 2, sd=1) == ALIGN
+    assert call(w=None) == BAD and call(wd=2) == BAD and call(rstd=None) == BAD and call(rstd=4 * P + 1) == ALIGN
+    assert call(lddh=63) == BAD and call(dh=5 * P + 1) == ALIGN
+    assert call(dx=None) == BAD and call(lddx=63) == BAD and call(dd=2) == BAD
+    assert call(dw=7 * P + 2) == ALIGN and call(work=None) == BAD and call(work=8 * P + 4) == ALIGN
+    assert call(rows=-1) == BAD and call(cols=40000, ldg=40000, ldh=40000, lddh=40000, lddx=40000) == UNSUP
+    assert call(cols=0) == OK and call(rows=0, dw=None) == OK
+    W = L.ufp4_rmsnorm_backward_workspace
+    assert W(0, 64) == 0 and W(5, 0) == 0 and W(1, 2048) == 2048 * 4 and W(1, 64) == 4 * 64 * 4
