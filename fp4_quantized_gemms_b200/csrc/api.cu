@@ -8,9 +8,12 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <utility>
+#include <vector>
 
 #include "ufp4.h"
 #include "ufp4_internal.h"
@@ -392,6 +395,65 @@ ufp4_status_t check_matrix(const void *p, int32_t dtype, int64_t rows, int64_t c
 }
 
 bool act_valid(int32_t act) { return act >= UFP4_ACT_NONE && act <= UFP4_ACT_SILU; }
+
+// Arguments that both passes of the balance loss share.
+ufp4_status_t fill_balance(const void *logits, int64_t ld, int32_t dtype, int64_t tokens, int32_t experts, int32_t topk,
+                           const uint8_t *mask, float coef, BalanceArgs *a) {
+    if (tokens < 0 || experts < 1 || topk < 1 || coef != coef) return UFP4_ERR_INVALID_ARG;
+    if (experts > kBalanceMaxExperts || tokens > (int64_t(1) << 31) / 2 || topk > kBalanceMaxExperts)
+        return UFP4_ERR_UNSUPPORTED;
+    const ufp4_status_t s = check_matrix(logits, dtype, tokens, experts, ld);
+    if (s != UFP4_OK) return s;
+    memset(a, 0, sizeof(*a));
+    a->logits = logits;
+    a->mask = mask;
+    a->tokens = tokens;
+    a->ld = ld;
+    a->experts = experts;
+    a->topk = topk;
+    a->bf16 = dtype == UFP4_DTYPE_BF16;
+    a->vec = experts % 4 == 0 && row_vec(logits, dtype, ld, 4);
+    a->coef = coef;
+    return UFP4_OK;
+}
+
+// Every tensor of a gradient list; `clip`: destinations are checked too.
+ufp4_status_t check_tensors(const ufp4_tensor_t *t, int32_t n, bool clip) {
+    if (n < 0 || (n > 0 && t == nullptr)) return UFP4_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n; ++i) {
+        if (t[i].n < 0 || t[i].n > (int64_t(1) << 46)) return UFP4_ERR_INVALID_ARG;
+        if (!dtype_valid(t[i].src_dtype) || (clip && !dtype_valid(t[i].dst_dtype))) return UFP4_ERR_INVALID_ARG;
+        if (t[i].n == 0) continue;
+        if (t[i].src == nullptr || (clip && t[i].dst == nullptr)) return UFP4_ERR_INVALID_ARG;
+        if (!elem_aligned(t[i].src, t[i].src_dtype) || (clip && !elem_aligned(t[i].dst, t[i].dst_dtype)))
+            return UFP4_ERR_ALIGNMENT;
+        if (clip && t[i].dst == t[i].src && t[i].dst_dtype != t[i].src_dtype) return UFP4_ERR_INVALID_ARG;
+    }
+    if (clip) {   // destinations that overlap (the same tensor listed twice) would be scaled twice
+        std::vector<std::pair<uintptr_t, uintptr_t>> r;
+        r.reserve(static_cast<size_t>(n));
+        for (int32_t i = 0; i < n; ++i) {
+            const uintptr_t d = reinterpret_cast<uintptr_t>(t[i].dst);
+            if (t[i].n > 0) r.emplace_back(d, d + static_cast<uintptr_t>(t[i].n) * elem_bytes(t[i].dst_dtype));
+        }
+        std::sort(r.begin(), r.end());
+        for (size_t i = 1; i < r.size(); ++i)
+            if (r[i].first < r[i - 1].second) return UFP4_ERR_INVALID_ARG;
+    }
+    return UFP4_OK;
+}
+
+ufp4_status_t run_clip(const ufp4_tensor_t *tensors, int32_t n, bool clip, float max_norm, float *norm, void *work,
+                       void *stream) {
+    const ufp4_status_t s = check_tensors(tensors, n, clip);
+    if (s != UFP4_OK) return s;
+    if (norm == nullptr || work == nullptr) return UFP4_ERR_INVALID_ARG;
+    if (!elem_aligned(norm, UFP4_DTYPE_FP32) || !aligned16(work)) return UFP4_ERR_ALIGNMENT;
+    return launch_grad_clip(tensors, n, static_cast<double *>(work), clip, max_norm, norm,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? UFP4_OK
+               : UFP4_ERR_CUDA;
+}
 
 ufp4_status_t check_input(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t axis) {
     if (rows < 0 || cols < 0) return UFP4_ERR_INVALID_ARG;
@@ -980,6 +1042,82 @@ ufp4_status_t ufp4_rmsnorm_backward(const void *dy_dev, int64_t ld_dy, int32_t d
             (dh_dev == nullptr || row_vec(dh_dev, stream_dtype, ld_dh, 8)) && row_vec(dx_dev, dx_dtype, ld_dx, 8);
     a.vec_weight = cols % 8 == 0 && row_vec(weight_dev, weight_dtype, 0, 8);
     return launch_rmsnorm_backward(a, st) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
+}
+
+size_t ufp4_moe_balance_workspace(int32_t experts) {
+    if (experts < 1 || experts > kBalanceMaxExperts) return 0;
+    return static_cast<size_t>(kBalanceBlocks) * (2 * static_cast<size_t>(experts) + 1) * 4;
+}
+
+ufp4_status_t ufp4_moe_balance(const void *logits_dev, int64_t ld, int32_t dtype, int64_t tokens, int32_t experts,
+                               const int32_t *choices_dev, int32_t topk, const uint8_t *mask_dev, float coef,
+                               float *loss_dev, int64_t *counts_dev, int64_t *valid_tokens_dev,
+                               void *workspace_dev, void *stream) {
+    BalanceArgs a;
+    const ufp4_status_t s = fill_balance(logits_dev, ld, dtype, tokens, experts, topk, mask_dev, coef, &a);
+    if (s != UFP4_OK) return s;
+    if (loss_dev == nullptr || counts_dev == nullptr || valid_tokens_dev == nullptr || workspace_dev == nullptr ||
+        (choices_dev == nullptr && tokens > 0))
+        return UFP4_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(loss_dev) | reinterpret_cast<uintptr_t>(choices_dev)) & 3u) return UFP4_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(counts_dev) | reinterpret_cast<uintptr_t>(valid_tokens_dev)) & 7u)
+        return UFP4_ERR_ALIGNMENT;
+    if (!aligned16(workspace_dev)) return UFP4_ERR_ALIGNMENT;
+    a.choices = choices_dev;
+    a.part_prob = static_cast<float *>(workspace_dev);
+    a.part_count = reinterpret_cast<int32_t *>(a.part_prob + static_cast<int64_t>(kBalanceBlocks) * experts);
+    a.part_tokens = a.part_count + static_cast<int64_t>(kBalanceBlocks) * experts;
+    a.loss = loss_dev;
+    a.counts = counts_dev;
+    a.valid_tokens = valid_tokens_dev;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (tokens == 0) {
+        const bool ok = cudaMemsetAsync(loss_dev, 0, sizeof(float), st) == cudaSuccess &&
+                        cudaMemsetAsync(counts_dev, 0, sizeof(int64_t) * experts, st) == cudaSuccess &&
+                        cudaMemsetAsync(valid_tokens_dev, 0, sizeof(int64_t), st) == cudaSuccess;
+        return ok ? UFP4_OK : UFP4_ERR_CUDA;
+    }
+    return launch_moe_balance(a, false, st) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
+}
+
+ufp4_status_t ufp4_moe_balance_backward(const void *logits_dev, int64_t ld, int32_t dtype, int64_t tokens,
+                                        int32_t experts, int32_t topk, const uint8_t *mask_dev, float coef,
+                                        const int64_t *counts_dev, const int64_t *valid_tokens_dev,
+                                        const float *dloss_dev, void *dlogits_dev, int64_t ld_d, void *stream) {
+    BalanceArgs a;
+    ufp4_status_t s = fill_balance(logits_dev, ld, dtype, tokens, experts, topk, mask_dev, coef, &a);
+    if (s != UFP4_OK) return s;
+    s = check_matrix(dlogits_dev, dtype, tokens, experts, ld_d);
+    if (s != UFP4_OK) return s;
+    if (counts_dev == nullptr || valid_tokens_dev == nullptr || dloss_dev == nullptr) return UFP4_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(counts_dev) | reinterpret_cast<uintptr_t>(valid_tokens_dev)) & 7u) ||
+        !elem_aligned(dloss_dev, UFP4_DTYPE_FP32))
+        return UFP4_ERR_ALIGNMENT;
+    if (tokens == 0) return UFP4_OK;
+    a.counts_in = counts_dev;
+    a.valid_tokens_in = valid_tokens_dev;
+    a.dloss = dloss_dev;
+    a.dlogits = dlogits_dev;
+    a.ld_d = ld_d;
+    a.vec = a.vec && row_vec(dlogits_dev, dtype, ld_d, 4);
+    return launch_moe_balance(a, true, static_cast<cudaStream_t>(stream)) == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
+}
+
+size_t ufp4_grad_norm_workspace(int32_t n_tensors) {
+    const int64_t n = n_tensors > 0 ? n_tensors : 1;
+    const int64_t launches = (n + kClipTable - 1) / kClipTable;
+    return static_cast<size_t>(launches) * kClipBlocks * sizeof(double);
+}
+
+ufp4_status_t ufp4_grad_norm(const ufp4_tensor_t *tensors_host, int32_t n_tensors, float *norm_dev,
+                             void *workspace_dev, void *stream) {
+    return run_clip(tensors_host, n_tensors, false, 0.0f, norm_dev, workspace_dev, stream);
+}
+
+ufp4_status_t ufp4_grad_clip(const ufp4_tensor_t *tensors_host, int32_t n_tensors, float max_norm, float *norm_dev,
+                             void *workspace_dev, void *stream) {
+    if (!(max_norm >= 0.0f)) return UFP4_ERR_INVALID_ARG;
+    return run_clip(tensors_host, n_tensors, true, max_norm, norm_dev, workspace_dev, stream);
 }
 
 ufp4_status_t ufp4_grouped_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,

@@ -1766,20 +1766,6 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
     }
 }
 
-// Raises a kernel's dynamic shared memory limit, once per device (the
-// attribute belongs to the device's context).
-template <typename F>
-cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-    return e;
-}
-
 template <int GRID, bool ATOMS, bool LANES, bool EPI>
 cudaError_t launch_pair_epi(const GemmArgs &args, int num_sms, cudaStream_t stream) {
     using C = PairCfg<GRID, ATOMS, LANES>;

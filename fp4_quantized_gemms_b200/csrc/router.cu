@@ -1,0 +1,274 @@
+// router.cu -- balance loss of a mixture-of-experts router, with per-expert
+// counts and the gradient of the logits.
+//
+// For T valid tokens, E experts, k choices per token, p = softmax(logits):
+//     c_e = number of choices of expert e,   f_e = c_e / (k T),   P_e = (sum over tokens of p_te) / T
+//     loss = coef * E * sum_e f_e P_e
+//     dloss/dlogits_te = p_te (g_e - sum_j p_tj g_j),   g_e = coef * E * f_e / T    (f is a constant)
+//
+// balance_partial_kernel reads logits and choices once: G lanes share a token
+// and hold its E / G logits in registers (max, exp, sum by shuffles), the
+// probabilities are added up in fp32 registers over a lane's tokens, then over
+// the block, and each block writes one partial row; balance_finish_kernel adds
+// the rows in a fixed order, so the loss has the same bits every time (the
+// counts are integers).  balance_backward_kernel recomputes p from the logits
+// (one read, one write): HBM is the bound of both.
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "ufp4.h"
+#include "ufp4_elem.cuh"
+#include "ufp4_internal.h"
+
+namespace ufp4 {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+
+// Experts of a token: lane g of its G lanes holds J of them, in vectors of V
+// consecutive ones: expert V (g + G (j / V)) + j % V.
+template <int G, int V>
+__device__ __forceinline__ int expert_of(int g, int j) {
+    return V * (g + G * (j / V)) + j % V;
+}
+
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// Softmax of a token's logits in registers; experts beyond E and tokens that
+// do not count (`live` false) give 0.  -inf logits give 0; a row of nothing
+// but -inf gives 0 everywhere.  NaN stays NaN.
+template <int G, int J, int V, bool BF16>
+__device__ __forceinline__ void token_softmax(const BalanceArgs &a, int64_t token, int g, bool live, float (&p)[J]) {
+    const int64_t base = token * a.ld;
+#pragma unroll
+    for (int j = 0; j < J; j += V) {
+        const int e = expert_of<G, V>(g, j);
+        if constexpr (V == 4) {
+            const float4 q = (live && e < a.experts) ? load_quad(a.logits, base + e, BF16, true, 4)
+                                                     : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+            p[j] = q.x, p[j + 1] = q.y, p[j + 2] = q.z, p[j + 3] = q.w;
+        } else {
+            p[j] = (live && e < a.experts) ? load_elem(a.logits, base + e, BF16) : -CUDART_INF_F;
+        }
+    }
+    float m = -CUDART_INF_F;
+#pragma unroll
+    for (int j = 0; j < J; ++j) m = fmaxf(m, p[j]);
+    m = group_max<G>(m);
+    const float shift = m == -CUDART_INF_F ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        p[j] = __expf(p[j] - shift);
+        s += p[j];
+    }
+    s = group_sum<G>(s);
+    const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
+#pragma unroll
+    for (int j = 0; j < J; ++j) p[j] *= inv;
+}
+
+template <int G, int J, int V, bool BF16>
+__global__ void __launch_bounds__(kThreads) balance_partial_kernel(const __grid_constant__ BalanceArgs a) {
+    extern __shared__ uint32_t s_mem[];
+    const int E = a.experts;
+    int32_t *s_count = reinterpret_cast<int32_t *>(s_mem);          // [E]
+    float *s_prob = reinterpret_cast<float *>(s_mem + E);           // [kWarps][E]
+    __shared__ int32_t s_tokens;
+    for (int i = threadIdx.x; i < E; i += kThreads) s_count[i] = 0;
+    if (threadIdx.x == 0) s_tokens = 0;
+    __syncthreads();
+    constexpr int kGroups = kThreads / G;                           // tokens of a block at a time
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = threadIdx.x % G;
+    float acc[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[j] = 0.0f;
+    int32_t mine = 0;
+    // whole warps go round together (the shuffles need all lanes)
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < a.tokens;
+         t0 += static_cast<int64_t>(gridDim.x) * kGroups) {
+        const int64_t t = t0 + threadIdx.x / G;
+        const bool live = t < a.tokens && (a.mask == nullptr || a.mask[t] != 0);
+        float p[J];
+        token_softmax<G, J, V, BF16>(a, t, g, live, p);
+#pragma unroll
+        for (int j = 0; j < J; ++j) acc[j] += p[j];
+        if (live) {
+            mine += g == 0;
+            for (int i = g; i < a.topk; i += G) {
+                const int e = a.choices[t * a.topk + i];
+                if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
+            }
+        }
+    }
+    // over the warp's token groups, then (in order) over the warps
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int o = G; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
+        const int e = expert_of<G, V>(g, j);
+        if (lane < G && e < E) s_prob[warp * E + e] = acc[j];
+    }
+    if (mine != 0) atomicAdd(&s_tokens, mine);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        float s = 0.0f;
+        for (int w = 0; w < kWarps; ++w) s += s_prob[w * E + e];
+        a.part_prob[static_cast<int64_t>(blockIdx.x) * E + e] = s;
+        a.part_count[static_cast<int64_t>(blockIdx.x) * E + e] = s_count[e];
+    }
+    if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = s_tokens;
+}
+
+// One block: adds the partial rows, writes counts, the token count and the loss.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_constant__ BalanceArgs a, int blocks) {
+    __shared__ double s_red[32];
+    __shared__ int64_t s_tok[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t tok = 0;
+    for (int b = threadIdx.x; b < blocks; b += 1024) tok += a.part_tokens[b];
+    double dot = 0.0;       // sum over this thread's experts of c_e * sum p_e
+    for (int e = threadIdx.x; e < a.experts; e += 1024) {
+        float s = 0.0f;
+        int64_t c = 0;
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) {
+            s += a.part_prob[static_cast<int64_t>(b) * a.experts + e];
+            c += a.part_count[static_cast<int64_t>(b) * a.experts + e];
+        }
+        a.counts[e] = c;
+        dot += static_cast<double>(c) * static_cast<double>(s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        tok += __shfl_xor_sync(0xFFFFFFFFu, tok, o);
+    }
+    if (lane == 0) {
+        s_red[warp] = dot;
+        s_tok[warp] = tok;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double d = 0.0;
+        int64_t n = 0;
+        for (int w = 0; w < 32; ++w) {
+            d += s_red[w];
+            n += s_tok[w];
+        }
+        *a.valid_tokens = n;
+        const double nn = static_cast<double>(n);
+        *a.loss = n == 0 ? 0.0f
+                         : static_cast<float>(static_cast<double>(a.coef) * a.experts * d / (nn * nn * a.topk));
+    }
+}
+
+template <int G, int J, int V, bool BF16>
+__global__ void __launch_bounds__(kThreads) balance_backward_kernel(const __grid_constant__ BalanceArgs a) {
+    constexpr int kGroups = kThreads / G;
+    const int g = threadIdx.x % G;
+    const int E = a.experts;
+    const double n = static_cast<double>(*a.valid_tokens_in);
+    const float scale = n == 0.0 ? 0.0f
+                                 : static_cast<float>(static_cast<double>(*a.dloss) * a.coef * E / (n * n * a.topk));
+    float ge[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int e = expert_of<G, V>(g, j);
+        ge[j] = e < E ? scale * static_cast<float>(a.counts_in[e]) : 0.0f;
+    }
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < a.tokens;
+         t0 += static_cast<int64_t>(gridDim.x) * kGroups) {
+        const int64_t t = t0 + threadIdx.x / G;
+        const bool in = t < a.tokens;
+        const bool live = in && (a.mask == nullptr || a.mask[t] != 0);
+        float p[J];
+        token_softmax<G, J, V, BF16>(a, t, g, live, p);
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) dot = fmaf(p[j], ge[j], dot);
+        dot = group_sum<G>(dot);
+#pragma unroll
+        for (int j = 0; j < J; j += V) {
+            const int e = expert_of<G, V>(g, j);
+            if (in && e < E) {
+                if constexpr (V == 4)
+                    store_quad(a.dlogits, t * a.ld_d + e, BF16, true, 4,
+                               make_float4(p[j] * (ge[j] - dot), p[j + 1] * (ge[j + 1] - dot),
+                                           p[j + 2] * (ge[j + 2] - dot), p[j + 3] * (ge[j + 3] - dot)));
+                else
+                    store_elem(a.dlogits, t * a.ld_d + e, BF16, p[j] * (ge[j] - dot));
+            }
+        }
+    }
+}
+
+template <int G, int J, int V, bool BF16>
+cudaError_t launch_shape(const BalanceArgs &a, bool backward, cudaStream_t stream) {
+    const int64_t groups = kThreads / G;
+    const int64_t need = (a.tokens + groups - 1) / groups;
+    if (backward) {
+        const int64_t most = int64_t(148) * 4;
+        balance_backward_kernel<G, J, V, BF16>
+            <<<static_cast<unsigned>(need < most ? need : most), kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    const int blocks = static_cast<int>(need < kBalanceBlocks ? need : kBalanceBlocks);
+    const int smem = a.experts * 4 * (1 + kWarps);
+    static std::atomic<uint64_t> done{0};
+    if (smem > 48 * 1024 - 256) {
+        const cudaError_t e = allow_smem(balance_partial_kernel<G, J, V, BF16>, 4 * kBalanceMaxExperts * (1 + kWarps), done);
+        if (e != cudaSuccess) return e;
+    }
+    balance_partial_kernel<G, J, V, BF16><<<blocks, kThreads, smem, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    balance_finish_kernel<<<1, 1024, 0, stream>>>(a, blocks);
+    return cudaGetLastError();
+}
+
+// Experts to lanes.  Rows that allow vectors of four: the fewest lanes that
+// leave each at most four (E <= 128), then a warp with more; else one expert
+// at a time.
+template <bool BF16>
+cudaError_t launch_type(const BalanceArgs &a, bool backward, cudaStream_t stream) {
+    const int E = a.experts;
+    if (a.vec) {
+        if (E <= 8) return launch_shape<2, 4, 4, BF16>(a, backward, stream);
+        if (E <= 16) return launch_shape<4, 4, 4, BF16>(a, backward, stream);
+        if (E <= 32) return launch_shape<8, 4, 4, BF16>(a, backward, stream);
+        if (E <= 64) return launch_shape<16, 4, 4, BF16>(a, backward, stream);
+        if (E <= 128) return launch_shape<32, 4, 4, BF16>(a, backward, stream);
+        if (E <= 256) return launch_shape<32, 8, 4, BF16>(a, backward, stream);
+        return launch_shape<32, 32, 4, BF16>(a, backward, stream);
+    }
+    if (E <= 8) return launch_shape<8, 1, 1, BF16>(a, backward, stream);
+    if (E <= 32) return launch_shape<32, 1, 1, BF16>(a, backward, stream);
+    if (E <= 128) return launch_shape<32, 4, 1, BF16>(a, backward, stream);
+    if (E <= 256) return launch_shape<32, 8, 1, BF16>(a, backward, stream);
+    return launch_shape<32, 32, 1, BF16>(a, backward, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_balance(const BalanceArgs &a, bool backward, cudaStream_t stream) {
+    return a.bf16 ? launch_type<true>(a, backward, stream) : launch_type<false>(a, backward, stream);
+}
+
+}  // namespace ufp4

@@ -5,9 +5,25 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ufp4.h"
 
 namespace ufp4 {
+
+// Raises a kernel's dynamic shared memory limit, once per device (the
+// attribute belongs to the device's context).
+template <typename F>
+cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Bits of the device error word: a bounded wait of that role gave up
 // (kernels OR them in; the host reads and clears the word in
@@ -219,6 +235,47 @@ struct NormBwdArgs {
 };
 int64_t rmsnorm_backward_slots(int64_t rows, int64_t cols);
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs &a, cudaStream_t stream);
+
+// Balance loss of a router (router.cu).  vec: experts % 4 == 0 and rows that
+// allow accesses of four elements.
+constexpr int kBalanceMaxExperts = 1024;
+constexpr int kBalanceBlocks = 148 * 2;   // partial rows of the forward pass, at most
+struct BalanceArgs {
+    const void *logits;          // [tokens][ld]
+    const int32_t *choices;      // [tokens][topk]
+    const uint8_t *mask;         // [tokens] or nullptr
+    float *part_prob;            // [blocks][experts]
+    int32_t *part_count;         // [blocks][experts]
+    int32_t *part_tokens;        // [blocks]
+    float *loss;
+    int64_t *counts, *valid_tokens;
+    const int64_t *counts_in, *valid_tokens_in;   // backward
+    const float *dloss;
+    void *dlogits;               // [tokens][ld_d]
+    int64_t tokens, ld, ld_d;
+    int32_t experts, topk, bf16, vec;
+    float coef;
+};
+cudaError_t launch_moe_balance(const BalanceArgs &a, bool backward, cudaStream_t stream);
+
+// Gradient norm and clipping (clip.cu): the tensors' addresses travel in the
+// kernel's parameters, up to kClipTable of them per launch.
+constexpr int kClipTable = 512;
+constexpr int kClipBlocks = 148 * 8;      // blocks (and fp64 sums) per launch, at most
+struct ClipEntry {
+    const void *src;
+    void *dst;
+    int64_t n, chunk0;           // elements, first chunk
+    uint8_t src_bf16, dst_bf16, vec;
+};
+template <int MAX>
+struct ClipTable {
+    int64_t chunks;
+    int32_t n;
+    ClipEntry e[MAX];
+};
+cudaError_t launch_grad_clip(const ufp4_tensor_t *tensors, int32_t n, double *sums, bool scale, float max_norm,
+                             float *norm, cudaStream_t stream);
 
 // Driver entry point for tensor-map encoding (resolved once at run time).
 CUresult encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base,

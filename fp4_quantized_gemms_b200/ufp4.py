@@ -8,6 +8,7 @@ that launches work raises if the tensors are not on a CUDA device.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass, replace
@@ -37,6 +38,8 @@ EXPORTED = [
     "ufp4_sf_atoms_layout", "ufp4_sf_lanes_layout", "ufp4_test_set_quantize_wait_limit",
     "ufp4_gemm_epilogue", "ufp4_epilogue_backward", "ufp4_epilogue_backward_workspace",
     "ufp4_rmsnorm", "ufp4_rmsnorm_backward", "ufp4_rmsnorm_backward_workspace",
+    "ufp4_moe_balance", "ufp4_moe_balance_backward", "ufp4_moe_balance_workspace",
+    "ufp4_grad_norm", "ufp4_grad_clip", "ufp4_grad_norm_workspace",
 ]
 
 
@@ -70,6 +73,11 @@ class EpilogueC(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("pre", ctypes.c_void_p),
                 ("ld_residual", ctypes.c_int64), ("ld_pre", ctypes.c_int64), ("bias_dtype", ctypes.c_int32),
                 ("residual_dtype", ctypes.c_int32), ("pre_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class TensorC(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
 
 
 class QStatsC(ctypes.Structure):
@@ -144,6 +152,18 @@ def lib() -> ctypes.CDLL:
         L.ufp4_rmsnorm_backward.restype = st
         L.ufp4_rmsnorm_backward.argtypes = [P, i64, i32, P, i64, i32, P, i32, P, P, i64, i64, i64, P, i64, i32, P,
                                             P, P]
+        L.ufp4_moe_balance_workspace.restype = ctypes.c_size_t
+        L.ufp4_moe_balance_workspace.argtypes = [i32]
+        L.ufp4_moe_balance.restype = st
+        L.ufp4_moe_balance.argtypes = [P, i64, i32, i64, i32, P, i32, P, f32, P, P, P, P, P]
+        L.ufp4_moe_balance_backward.restype = st
+        L.ufp4_moe_balance_backward.argtypes = [P, i64, i32, i64, i32, i32, P, f32, P, P, P, P, i64, P]
+        L.ufp4_grad_norm_workspace.restype = ctypes.c_size_t
+        L.ufp4_grad_norm_workspace.argtypes = [i32]
+        L.ufp4_grad_norm.restype = st
+        L.ufp4_grad_norm.argtypes = [P, i32, P, P, P]
+        L.ufp4_grad_clip.restype = st
+        L.ufp4_grad_clip.argtypes = [P, i32, f32, P, P, P]
         L.ufp4_check_device_status.restype = st
         L.ufp4_check_device_status.argtypes = []
         L.ufp4_sf_atoms_layout.restype = st
@@ -688,6 +708,103 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
           _dtype(weight, "weight"), rstd.data_ptr(), _ptr(dh), lddh, rows, cols, dx.data_ptr(), lddx, dd,
           _ptr(dweight), _ptr(work))
     return dx, dweight
+
+
+def _mask_ptr(mask: torch.Tensor | None, tokens: int):
+    if mask is None:
+        return None
+    _need(mask.dtype in (torch.bool, torch.uint8), "mask: bool or uint8")
+    _vector(mask, tokens, "mask")
+    return mask.data_ptr()
+
+
+def moe_balance(logits: torch.Tensor, experts: torch.Tensor, coef: float = 1.0, mask: torch.Tensor | None = None):
+    """Balance loss of a router: (loss [1] float32, counts [E] int64, valid
+    tokens [1] int64).  logits [tokens, E] bfloat16 or float32; experts
+    [tokens, k] int32, the chosen experts (an index outside [0, E) is a
+    dropped choice); mask [tokens], False for tokens that do not count."""
+    _require_cuda(logits, experts, mask)
+    device = logits.device
+    _same_device(device, experts, mask)
+    _need(logits.dim() == 2, "logits: a matrix")
+    tokens, n = logits.shape
+    dt, ld = _dtype(logits, "logits"), _pitch(logits, tokens, n, "logits")
+    _need(experts.dtype == torch.int32 and experts.dim() == 2 and experts.shape[0] == tokens and
+          experts.is_contiguous(), "experts: a contiguous int32 matrix, a row per token")
+    mp = _mask_ptr(mask, tokens)
+    loss = torch.empty(1, dtype=torch.float32, device=device)
+    counts = torch.empty(n, dtype=torch.int64, device=device)
+    valid = torch.empty(1, dtype=torch.int64, device=device)
+    work = torch.empty(lib().ufp4_moe_balance_workspace(n), dtype=torch.uint8, device=device)
+    _call("ufp4_moe_balance", device, logits.data_ptr(), ld, dt, tokens, n, experts.data_ptr(), experts.shape[1], mp,
+          coef, loss.data_ptr(), counts.data_ptr(), valid.data_ptr(), work.data_ptr())
+    return loss, counts, valid
+
+
+def moe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, dloss: torch.Tensor,
+                         topk: int, coef: float = 1.0, mask: torch.Tensor | None = None,
+                         dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of moe_balance's loss with respect to the logits.  counts and
+    tokens (the number that count) are moe_balance's results, topk the
+    choices per token, dloss [1] float32 the loss's own gradient."""
+    _require_cuda(logits, counts, tokens, dloss, mask, dlogits)
+    device = logits.device
+    _same_device(device, counts, tokens, dloss, mask, dlogits)
+    _need(logits.dim() == 2, "logits: a matrix")
+    rows, n = logits.shape
+    dt, ld = _dtype(logits, "logits"), _pitch(logits, rows, n, "logits")
+    _need(counts.dtype == torch.int64 and tokens.dtype == torch.int64 and tokens.numel() == 1, "counts, tokens: int64")
+    _vector(counts, n, "counts")
+    _need(dloss.dtype == torch.float32 and dloss.numel() == 1, "dloss: one float32")
+    if dlogits is None:
+        dlogits = torch.empty((rows, n), dtype=logits.dtype, device=device)
+    _need(dlogits.dtype == logits.dtype, "dlogits: the logits' type")
+    ldd = _pitch(dlogits, rows, n, "dlogits")
+    _call("ufp4_moe_balance_backward", device, logits.data_ptr(), ld, dt, rows, n, topk, _mask_ptr(mask, rows), coef,
+          counts.data_ptr(), tokens.data_ptr(), dloss.data_ptr(), dlogits.data_ptr(), ldd)
+    return dlogits
+
+
+def _tensor_table(grads, out):
+    """ufp4_tensor_t array of a gradient list (out: destinations, or None)."""
+    table, device = array.array("q"), None
+    for i, t in enumerate(grads):
+        o = t if out is None else out[i]
+        if device is None:
+            device = t.device
+        if not (t.is_cuda and o.is_cuda):
+            raise RuntimeError("ufp4 kernels need CUDA tensors (there is no CPU path)")
+        if t.device != device or o.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: one call works on one device")
+        if not (t.is_contiguous() and o.is_contiguous()) or t.numel() != o.numel():
+            raise ValueError(f"gradient {i}: contiguous tensors, a destination of the same size")
+        table.extend((t.data_ptr(), o.data_ptr(), t.numel(), _dtype(t, "gradient") | _dtype(o, "out") << 32))
+    return table, device
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """Global norm of a list of gradients (bfloat16 or float32, contiguous):
+    float32 [1] on their device."""
+    table, device = _tensor_table(grads, None)
+    _need(device is not None, "grads: at least one tensor")
+    norm = torch.empty(1, dtype=torch.float32, device=device)
+    work = torch.empty(lib().ufp4_grad_norm_workspace(len(grads)), dtype=torch.uint8, device=device)
+    _call("ufp4_grad_norm", device, table.buffer_info()[0], len(grads), norm.data_ptr(), work.data_ptr())
+    return norm
+
+
+def grad_clip(grads, max_norm: float, out=None) -> torch.Tensor:
+    """Clips a list of gradients to a global norm of max_norm, in place or into
+    the tensors of `out` (same sizes, bfloat16 or float32); returns the norm
+    before clipping, float32 [1].  A norm that is not finite leaves the values
+    as they are."""
+    _need(out is None or len(out) == len(grads), "out: a tensor for each gradient")
+    table, device = _tensor_table(grads, out)
+    _need(device is not None, "grads: at least one tensor")
+    norm = torch.empty(1, dtype=torch.float32, device=device)
+    work = torch.empty(lib().ufp4_grad_norm_workspace(len(grads)), dtype=torch.uint8, device=device)
+    _call("ufp4_grad_clip", device, table.buffer_info()[0], len(grads), max_norm, norm.data_ptr(), work.data_ptr())
+    return norm
 
 
 GEMM_PATH_AUTO, GEMM_PATH_NATIVE_FP4, GEMM_PATH_NATIVE_FP4_PAIR256 = 0, 3, 5

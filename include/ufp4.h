@@ -26,7 +26,10 @@
  *   6. What a training step runs around those products: ufp4_gemm_epilogue
  *      (bias, activation and residual in the GEMM's epilogue) and
  *      ufp4_rmsnorm (RMS norm of the residual stream, bf16 or 8-bit operand
- *      out), each with its backward pass.  No counterpart on the pages.
+ *      out), each with its backward pass; ufp4_moe_balance (balance loss and
+ *      per-expert counts of a router) with its gradient; ufp4_grad_norm and
+ *      ufp4_grad_clip (global norm and clipping of many gradients).  No
+ *      counterpart on the pages.
  *
  * Conventions shared by every call:
  *   - All pointers named *_dev, and every pointer inside ufp4_qtensor_t, are
@@ -449,6 +452,69 @@ ufp4_status_t ufp4_rmsnorm_backward(const void *dy_dev, int64_t ld_dy, int32_t d
                                     int32_t weight_dtype, const float *rstd_dev, const void *dh_dev, int64_t ld_dh,
                                     int64_t rows, int64_t cols, void *dx_dev, int64_t ld_dx, int32_t dx_dtype,
                                     float *dweight_dev, void *workspace_dev, void *stream);
+
+/* Balance loss of a mixture-of-experts router, and its per-expert counts (the
+ * rows of a grouped GEMM's groups).  For the T tokens that count, p =
+ * softmax(logits) over E experts, k choices per token:
+ *   counts[e] = choices of expert e;  f_e = counts[e] / (k T);  P_e = mean of p_te
+ *   loss = coef * E * sum_e f_e P_e           (0 when no token counts)
+ *   logits_dev   [tokens][ld] of dtype.  -inf leaves an expert out (p = 0); a
+ *                row of nothing but -inf adds nothing to P.
+ *   choices_dev  int32 [tokens][topk], contiguous; an index outside [0, E) (a
+ *                dropped choice) is not counted; an index may repeat.
+ *   mask_dev     u8 [tokens] (0: the token does not count), or NULL.
+ *   loss_dev     fp32; counts_dev int64 [experts]; valid_tokens_dev int64: T.
+ *   workspace_dev  ufp4_moe_balance_workspace(experts) bytes, 16-byte aligned,
+ *                used during the call only; calls that may run at the same
+ *                time need one each.
+ * The sums are added in a fixed order.  Errors: INVALID_ARG, ALIGNMENT,
+ * UNSUPPORTED (experts > 1024), CUDA. */
+size_t ufp4_moe_balance_workspace(int32_t experts);
+ufp4_status_t ufp4_moe_balance(const void *logits_dev, int64_t ld, int32_t dtype, int64_t tokens, int32_t experts,
+                               const int32_t *choices_dev, int32_t topk, const uint8_t *mask_dev, float coef,
+                               float *loss_dev, int64_t *counts_dev, int64_t *valid_tokens_dev,
+                               void *workspace_dev, void *stream);
+
+/* Gradient of the balance loss with respect to the logits (counts and T as
+ * the forward wrote them are constants):
+ *   dlogits = p (g - sum_j p_j g_j),  g_e = dloss * coef * E * counts[e] / (k T^2)
+ * dlogits_dev [tokens][ld_d] of dtype, all written (0 for tokens that do not
+ * count); it may be the logits (same pitch).  dloss_dev: fp32 on the device.
+ * Errors: as ufp4_moe_balance. */
+ufp4_status_t ufp4_moe_balance_backward(const void *logits_dev, int64_t ld, int32_t dtype, int64_t tokens,
+                                        int32_t experts, int32_t topk, const uint8_t *mask_dev, float coef,
+                                        const int64_t *counts_dev, const int64_t *valid_tokens_dev,
+                                        const float *dloss_dev, void *dlogits_dev, int64_t ld_d, void *stream);
+
+/* One gradient tensor of ufp4_grad_norm / ufp4_grad_clip: n contiguous
+ * elements.  dst may be src (same type: in place), but may not overlap any
+ * other tensor of the call. */
+typedef struct {
+    const void *src;
+    void *dst;               /* ufp4_grad_clip only                           */
+    int64_t n;
+    int32_t src_dtype;       /* ufp4_dtype_t                                  */
+    int32_t dst_dtype;       /* ufp4_dtype_t; ufp4_grad_clip only             */
+} ufp4_tensor_t;
+
+/* Global norm of many gradients, N = sqrt(sum of all squares) (fp64 inside),
+ * and clipping: dst = src * min(1, max_norm / N), rounded once.
+ *   tensors_host  array of n_tensors in host memory, read before the call
+ *                 returns (a captured call keeps the addresses it saw).
+ *   norm_dev      fp32, receives N.
+ *   workspace_dev ufp4_grad_norm_workspace(n_tensors) bytes, 16-byte aligned,
+ *                 used during the call only; calls that may run at the same
+ *                 time need one each.
+ * A NaN or an infinity among the gradients makes N NaN or infinite; then
+ * nothing is scaled (dst = src).  (A finite N beyond fp32's range is reported
+ * as infinity, and the gradients are scaled by it.)  The sums are added in a
+ * fixed order.  Errors: INVALID_ARG (a negative or NaN max_norm, two
+ * destinations that overlap, among others), ALIGNMENT, CUDA. */
+size_t ufp4_grad_norm_workspace(int32_t n_tensors);
+ufp4_status_t ufp4_grad_norm(const ufp4_tensor_t *tensors_host, int32_t n_tensors, float *norm_dev,
+                             void *workspace_dev, void *stream);
+ufp4_status_t ufp4_grad_clip(const ufp4_tensor_t *tensors_host, int32_t n_tensors, float max_norm, float *norm_dev,
+                             void *workspace_dev, void *stream);
 
 /* Kernel family for GEMMs whose operands carry two-level (E4M3 x fp32)
  * scales.  Both families run the block-scaled FP4 MMA (kind::mxf4nvf4, UE4M3

@@ -32,7 +32,7 @@ def _layout_of(tmp_path, struct, fields):
     return list(map(int, subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()))
 
 
-@pytest.mark.parametrize("struct,mirror", [("ufp4_epilogue_t", "EpilogueC")])
+@pytest.mark.parametrize("struct,mirror", [("ufp4_epilogue_t", "EpilogueC"), ("ufp4_tensor_t", "TensorC")])
 def test_struct_layouts(tmp_path, struct, mirror):
     c = getattr(ufp4, mirror)
     names = [f[0] for f in c._fields_]
@@ -177,3 +177,53 @@ def test_rmsnorm_backward(L):
     assert call(cols=0) == OK and call(rows=0, dw=None) == OK
     W = L.ufp4_rmsnorm_backward_workspace
     assert W(0, 64) == 0 and W(5, 0) == 0 and W(1, 2048) == 2048 * 4 and W(1, 64) == 4 * 64 * 4
+
+
+def test_moe_balance(L):
+    def fwd(x=P, ld=64, dt=0, t=100, e=64, c=2 * P, k=2, mask=None, coef=1.0, loss=3 * P, counts=4 * P, valid=5 * P,
+            work=6 * P):
+        return L.ufp4_moe_balance(x, ld, dt, t, e, c, k, mask, coef, loss, counts, valid, work, None)
+
+    assert fwd(x=None) == BAD and fwd(ld=63) == BAD and fwd(dt=2) == BAD and fwd(x=P + 1) == ALIGN
+    assert fwd(t=-1) == BAD and fwd(e=0) == BAD and fwd(k=0) == BAD and fwd(coef=float("nan")) == BAD
+    assert fwd(e=1025, ld=1025) == UNSUP and fwd(k=1025) == UNSUP and fwd(t=1 << 31) == UNSUP
+    assert fwd(c=None) == BAD and fwd(loss=None) == BAD and fwd(counts=None) == BAD and fwd(valid=None) == BAD
+    assert fwd(work=None) == BAD and fwd(work=6 * P + 8) == ALIGN
+    assert fwd(c=2 * P + 2) == ALIGN and fwd(loss=3 * P + 2) == ALIGN and fwd(counts=4 * P + 4) == ALIGN
+    assert fwd(valid=5 * P + 4) == ALIGN
+
+    def bwd(x=P, ld=64, dt=0, t=100, e=64, k=2, mask=None, coef=1.0, counts=4 * P, valid=5 * P, dl=6 * P, d=7 * P,
+            ldd=64):
+        return L.ufp4_moe_balance_backward(x, ld, dt, t, e, k, mask, coef, counts, valid, dl, d, ldd, None)
+
+    assert bwd(x=None) == BAD and bwd(ld=63) == BAD and bwd(dt=3) == BAD and bwd(e=0) == BAD and bwd(k=0) == BAD
+    assert bwd(e=2000, ld=2000, ldd=2000) == UNSUP
+    assert bwd(counts=None) == BAD and bwd(valid=None) == BAD and bwd(dl=None) == BAD and bwd(d=None) == BAD
+    assert bwd(ldd=63) == BAD and bwd(d=7 * P + 1) == ALIGN and bwd(counts=4 * P + 4) == ALIGN
+    assert bwd(dl=6 * P + 2) == ALIGN and bwd(t=0) == OK
+    W = L.ufp4_moe_balance_workspace
+    assert W(0) == 0 and W(1025) == 0 and W(64) > 0
+
+
+def test_grad_clip(L):
+    def table(*rows):
+        return (ufp4.TensorC * len(rows))(*[ufp4.TensorC(*r) for r in rows])
+
+    def clip(t, n=None, max_norm=1.0, norm=P, work=2 * P):
+        return L.ufp4_grad_clip(t, len(t) if n is None else n, max_norm, norm, work, None)
+
+    good = (4 * P, 4 * P, 100, 1, 1)
+    assert clip(table(good), n=-1) == BAD and L.ufp4_grad_clip(None, 1, 1.0, P, 2 * P, None) == BAD
+    assert clip(table(good), max_norm=-1.0) == BAD and clip(table(good), max_norm=float("nan")) == BAD
+    assert clip(table(good), norm=None) == BAD and clip(table(good), work=None) == BAD
+    assert clip(table(good), norm=P + 2) == ALIGN and clip(table(good), work=2 * P + 8) == ALIGN
+    assert clip(table(good, (None, 8 * P, 10, 1, 1))) == BAD and clip(table((4 * P, None, 10, 1, 1))) == BAD
+    assert clip(table((4 * P, 4 * P, -1, 1, 1))) == BAD and clip(table((4 * P, 8 * P, 10, 2, 1))) == BAD
+    assert clip(table((4 * P, 8 * P, 10, 1, 7))) == BAD and clip(table((4 * P, 4 * P, 10, 1, 0))) == BAD
+    assert clip(table((4 * P + 2, 8 * P, 10, 1, 1))) == ALIGN and clip(table((4 * P, 8 * P + 1, 10, 1, 0))) == ALIGN
+    assert clip(table(good, good)) == BAD                                           # listed twice
+    assert clip(table(good, (9 * P, 4 * P + 396, 5, 0, 1))) == BAD                  # overlap by one element
+    assert L.ufp4_grad_norm(table((4 * P, None, 10, 5, 0)), 1, P, 2 * P, None) == BAD
+    assert L.ufp4_grad_norm(table((4 * P + 1, None, 10, 0, 0)), 1, P, 2 * P, None) == ALIGN
+    W = L.ufp4_grad_norm_workspace
+    assert W(0) == W(1) == W(512) and W(513) == 2 * W(1) and W(1) % 8 == 0
