@@ -22,6 +22,7 @@ namespace ufp4 {
 
 cudaError_t read_and_clear_error_word(uint32_t *out);            // gemm.cu
 cudaError_t quantize_read_and_clear_error_word(uint32_t *out);   // quantize.cu
+cudaError_t norm_read_and_clear_error_word(uint32_t *out);       // norm.cu
 cudaError_t quantize_set_producer_wait_limit(uint64_t limit_ns);  // quantize.cu
 
 namespace {
@@ -164,6 +165,8 @@ ufp4_status_t check_pair(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b, bool 
 
 std::atomic<int32_t> g_two_level_path{UFP4_GEMM_PATH_AUTO};
 
+// Tensor maps of an operand's codes and block-major scales; a null map is not
+// needed by the chosen kernel (encoding one costs about a microsecond).
 ufp4_status_t encode_operand_maps(const ufp4_qtensor_t *q, int code_rows, int scale_rows, int mode, int k_stage,
                                   CUtensorMap *codes, CUtensorMap *scales) {
     const int64_t rows_t = q->rows > 0 ? q->rows : 1;
@@ -175,11 +178,12 @@ ufp4_status_t encode_operand_maps(const ufp4_qtensor_t *q, int code_rows, int sc
                                    : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
     CUresult r = CUDA_SUCCESS;
-    if (q->cfg.grid != UFP4_GRID_E4M3)   // 8-bit operands have no codes (their elements have their own map)
+    if (codes != nullptr)
         r = encode_tensor_map_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, q->codes, static_cast<uint64_t>(q->kpad / 2),
                                  static_cast<uint64_t>(rows_t), static_cast<uint64_t>(q->kpad / 2), row_bytes,
                                  static_cast<uint32_t>(code_rows), swz);
     if (r != CUDA_SUCCESS) return UFP4_ERR_CUDA;
+    if (scales == nullptr) return UFP4_OK;
     const int nblk_stage = k_stage / q->cfg.block;
     const uint64_t nblk = static_cast<uint64_t>(q->kpad / q->cfg.block);
     if (mode != 0 || q->cfg.scale_fmt == UFP4_SCALE_UE8M0) {   // byte scales
@@ -268,9 +272,14 @@ ufp4_status_t run_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
     const int grid_kind = a->cfg.grid == UFP4_GRID_E1M2 ? 0 : 1;
     // K elements per pipeline stage of the chosen kernel.
     const int k_stage = mode == 0 ? 64 : (mode == 5 ? pair_stage_k(grid_kind, use_atoms) : 128);
-    s = encode_operand_maps(a, 128, 128, mode, k_stage, &args.tm_a_codes, &args.tm_a_scales);
+    // The pair kernel reads E1M2 codes through the map over both planes, MX
+    // and 8-bit elements through their own, and atoms in place of scales.
+    const bool codes_map = mode != 6 && !(mode == 5 && grid_kind == 0);
+    s = encode_operand_maps(a, 128, 128, mode, k_stage, codes_map ? &args.tm_a_codes : nullptr,
+                            use_atoms ? nullptr : &args.tm_a_scales);
     if (s != UFP4_OK) return s;
-    s = encode_operand_maps(b, bn, bscale, mode, k_stage, &args.tm_b_codes, &args.tm_b_scales);
+    s = encode_operand_maps(b, bn, bscale, mode, k_stage, codes_map ? &args.tm_b_codes : nullptr,
+                            use_atoms ? nullptr : &args.tm_b_scales);
     if (s != UFP4_OK) return s;
     if (mode == 6) {   // E4M3 element planes: 128-byte rows (128 K per stage), 128-byte swizzle
         const int64_t ra = a->rows > 0 ? a->rows : 1, rb = b->rows > 0 ? b->rows : 1;
@@ -320,10 +329,9 @@ ufp4_status_t run_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
             ufp4_qtensor_t ac = *a, bc = *b;
             ac.codes = a->corr;
             bc.codes = b->corr;
-            CUtensorMap scratch;
-            s = encode_operand_maps(&ac, 128, 128, mode, k_stage, &args.tm_a_corr, &scratch);
+            s = encode_operand_maps(&ac, 128, 128, mode, k_stage, &args.tm_a_corr, nullptr);
             if (s != UFP4_OK) return s;
-            s = encode_operand_maps(&bc, bn, bscale, mode, k_stage, &args.tm_b_corr, &scratch);
+            s = encode_operand_maps(&bc, bn, bscale, mode, k_stage, &args.tm_b_corr, nullptr);
             if (s != UFP4_OK) return s;
         }
         args.corr_in = 1;
@@ -853,6 +861,8 @@ ufp4_status_t ufp4_gemm_epilogue(const ufp4_qtensor_t *a, const ufp4_qtensor_t *
             e.vec_pre = row_vec(epi->pre, epi->pre_dtype, epi->ld_pre, 4);
         }
     }
+    e.vec_all = e.vec_out && (e.bias == nullptr || e.vec_bias) && (e.residual == nullptr || e.vec_res) &&
+                (e.pre == nullptr || e.vec_pre);
     return run_gemm(a, b, nullptr, 0, nullptr, 0, m, n, stream, &e);
 }
 
@@ -1148,6 +1158,8 @@ ufp4_status_t ufp4_check_device_status(void) {
     if (read_and_clear_error_word(&w) != cudaSuccess) return UFP4_ERR_CUDA;
     uint32_t wq = 0;
     if (quantize_read_and_clear_error_word(&wq) != cudaSuccess) return UFP4_ERR_CUDA;
+    w |= wq;
+    if (norm_read_and_clear_error_word(&wq) != cudaSuccess) return UFP4_ERR_CUDA;
     w |= wq;
     return w == 0 ? UFP4_OK : UFP4_ERR_DEVICE_TIMEOUT;
 }

@@ -17,7 +17,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ufp4.h"
+#define UFP4_PIPELINE_KERNELS 1
+#include "ufp4_device.cuh"
 #include "ufp4_elem.cuh"
 #include "ufp4_internal.h"
 
@@ -88,14 +92,18 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sum over the W warps that share a row; every thread gets it.  `slot` holds
-// W floats of shared memory that no earlier sum still uses.
+// W floats of shared memory that no earlier sum still uses.  `bad` leaves as
+// true in every thread when it came as true in any.
 template <int W>
-__device__ __forceinline__ float row_sum(float v, float *slot) {
+__device__ __forceinline__ float row_sum(float v, float *slot, bool *bad = nullptr) {
     v = warp_sum(v);
     if constexpr (W > 1) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         if (lane == 0) slot[warp] = v;
-        __syncthreads();
+        if (bad == nullptr)
+            __syncthreads();
+        else
+            *bad = __syncthreads_or(*bad) != 0;
         v = slot[lane % W];
         // the W sums, each the same number of times in the 32 lanes
 #pragma unroll
@@ -133,6 +141,157 @@ struct RowShape {
     static constexpr int kThreads = kRowThreads * kRows;
 };
 
+// Writes eight columns of a row's output, y = h r w: bf16, or E4M3 elements and
+// their blocks' factors (all lanes of the warp take part: a block of 32
+// elements is four neighbouring lanes; elements beyond the row are 0).
+template <bool OUT8, bool VEC>
+__device__ __forceinline__ void write_y(const NormArgs &a, int64_t row, int64_t col, int valid, const float (&v)[8]) {
+    if constexpr (!OUT8) {
+        put8<true, VEC>(a.y, row * a.ld_y + col, valid, v);
+    } else {
+        float amax = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const int x = block_exponent(amax);
+        const float inv = exp2_neg(x);
+        if (col < a.kpad) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e] * inv, v[2 * e + 1] * inv), __NV_SATFINITE,
+                                                __NV_E4M3);
+            *reinterpret_cast<uint2 *>(a.elems8 + row * a.kpad + col) =
+                make_uint2(plain_zeros(p[0] | (p[1] << 16)), plain_zeros(p[2] | (p[3] << 16)));
+            if ((threadIdx.x & 3) == 0) {
+                const int64_t b = col / 32;
+                const uint8_t byte = static_cast<uint8_t>(x + 127);
+                a.scales[b * a.scale_ld + row] = byte;
+                if (a.sf_atoms != nullptr)
+                    a.sf_atoms[((row / 128) * a.atoms_k + b / 4) * 512 + 16 * (row % 32) + 4 * ((row / 32) % 4) +
+                               b % 4] = byte;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows through a ring in shared memory: bulk copies bring the next rows of the
+// block's tensors while the current one is reduced, so the reduction's
+// barriers and the second half of the row's work never leave HBM idle.  The
+// row sum's barrier is also what frees a stage: every thread has moved its
+// part of the row into registers by then, and thread 0 refills the stage.
+constexpr int kMaxStages = 8;
+
+__device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(smem_dst)),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+struct RingState {
+    uint64_t full[kMaxStages];
+    uint32_t abort;
+};
+
+// Waits (with a limit) for copies [from, to) to land, so that none is in
+// flight when the block ends early.
+__device__ __forceinline__ void drain_ring(RingState &s, int64_t from, int64_t to, int stages) {
+    uint32_t dummy = 0;
+    for (int64_t k = from; k < to; ++k)
+        mbar_wait(&s.full[k % stages], static_cast<uint32_t>(k / stages) & 1u, kErrTimeoutDrain, &dummy);
+}
+
+// Eight elements of a staged row.
+template <bool BF16>
+__device__ __forceinline__ void load8s(const uint8_t *p, int col, bool ok, float (&v)[8]) {
+    load8<BF16, true>(p, col, ok ? 8 : 0, v);
+}
+
+template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8>
+__global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ RingState st;
+    __shared__ float s_sum[2][W];
+    const int t = threadIdx.x;
+    const int cols = static_cast<int>(a.cols);
+    const uint32_t x_bytes = static_cast<uint32_t>(cols) * (XBF16 ? 2u : 4u);
+    const uint32_t r_bytes = RES ? static_cast<uint32_t>(cols) * (SBF16 ? 2u : 4u) : 0u;
+    const int64_t n = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;      // rows of this block
+    auto issue = [&](int64_t k) {
+        const int s = static_cast<int>(k % a.stages);
+        const int64_t row = blockIdx.x + k * gridDim.x;
+        uint8_t *buf = ring + s * a.stage_bytes;
+        mbar_arrive_expect_tx(&st.full[s], x_bytes + r_bytes);
+        bulk_load(buf, static_cast<const uint8_t *>(a.x) + row * a.ld_x * (XBF16 ? 2 : 4), x_bytes, &st.full[s]);
+        if constexpr (RES)
+            bulk_load(buf + x_bytes, static_cast<const uint8_t *>(a.residual) + row * a.ld_res * (SBF16 ? 2 : 4),
+                      r_bytes, &st.full[s]);
+    };
+    if (t == 0) {
+        for (int s = 0; s < a.stages; ++s) mbar_init(&st.full[s], 1);
+        st.abort = 0u;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (t == 0)
+        for (int64_t k = 0; k < a.stages && k < n; ++k) issue(k);
+    float w[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int col = 8 * (t + 32 * W * j);
+        load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, w[j]);
+    }
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    int s = 0;
+    uint32_t parity = 0;
+    bool bad = false;
+    int64_t k = 0;
+    for (; k < n; ++k) {
+        const int64_t row = blockIdx.x + k * gridDim.x;
+        bad = !mbar_wait(&st.full[s], parity, kErrTimeoutTransform, &st.abort);
+        const uint8_t *buf = ring + s * a.stage_bytes;
+        float h[NV][8];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = 8 * (t + 32 * W * j);
+            load8s<XBF16>(buf, col, col < cols, h[j]);
+            if constexpr (RES) {
+                float r[8];
+                load8s<SBF16>(buf + x_bytes, col, col < cols, r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    h[j][e] += r[e];
+                    if constexpr (SBF16) h[j][e] = __bfloat162float(__float2bfloat16_rn(h[j][e]));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(h[j][e], h[j][e], sum);
+        }
+        sum = row_sum<W>(sum, s_sum[k & 1], &bad);
+        if (bad) break;
+        if (t == 0 && k + a.stages < n) issue(k + a.stages);
+        const float rstd = 1.0f / sqrtf(sum * inv_cols + a.eps);
+        if (t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = 8 * (t + 32 * W * j);
+            if constexpr (RES) put8<SBF16, true>(a.h, row * a.ld_h + col, cols - col, h[j]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * rstd * w[j][e];
+            write_y<OUT8, true>(a, row, col, cols - col, h[j]);
+        }
+        if (++s == a.stages) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+    if (bad && t == 0) drain_ring(st, k, n < k + a.stages ? n : k + a.stages, a.stages);
+}
+
 template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8, bool VEC>
 __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     using S = RowShape<W>;
@@ -161,7 +320,7 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_kernel(const __
         for (int e = 0; e < 8; ++e) sum = fmaf(h[j][e], h[j][e], sum);
     }
     sum = row_sum<W>(sum, s_sum);
-    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+    const float rstd = 1.0f / sqrtf(sum * (1.0f / static_cast<float>(a.cols)) + a.eps);
     if (t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -171,42 +330,25 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_kernel(const __
         load_weight8(a.weight, a.weight_bf16, col, valid, a.vec_weight, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * rstd * w[e];
-        if constexpr (!OUT8) {
-            put8<true, VEC>(a.y, row * a.ld_y + col, valid, h[j]);
-        } else {
-            // blocks of 32 elements: four neighbouring lanes (all lanes of the
-            // warp take part; elements beyond the row are 0)
-            float amax = 0.0f;
+        write_y<OUT8, VEC>(a, row, col, valid, h[j]);
+    }
+}
+
+// The weight gradient of a block's rows, to its partial row.
+template <int W, int NV>
+__device__ __forceinline__ void write_partial(const NormBwdArgs &a, const float (&dw)[NV][8]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(h[j][e]));
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            const int x = block_exponent(amax);
-            const float inv = exp2_neg(x);
-            if (col < a.kpad) {
-                uint32_t p[4];
+    for (int j = 0; j < NV; ++j) {
+        const int64_t col = 8 * (threadIdx.x + 32 * W * j);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    p[e] = __nv_cvt_float2_to_fp8x2(make_float2(h[j][2 * e] * inv, h[j][2 * e + 1] * inv),
-                                                    __NV_SATFINITE, __NV_E4M3);
-                *reinterpret_cast<uint2 *>(a.elems8 + row * a.kpad + col) =
-                    make_uint2(plain_zeros(p[0] | (p[1] << 16)), plain_zeros(p[2] | (p[3] << 16)));
-                if ((t & 3) == 0) {
-                    const int64_t b = col / 32;
-                    const uint8_t byte = static_cast<uint8_t>(x + 127);
-                    a.scales[b * a.scale_ld + row] = byte;
-                    if (a.sf_atoms != nullptr)
-                        a.sf_atoms[((row / 128) * a.atoms_k + b / 4) * 512 + 16 * (row % 32) + 4 * ((row / 32) % 4) +
-                                   b % 4] = byte;
-                }
-            }
-        }
+        for (int e = 0; e < 8; ++e)
+            if (col + e < a.cols) a.partial[blockIdx.x * a.cols + col + e] = dw[j][e];
     }
 }
 
 // Backward: a block takes rows blockIdx.x * R + its row slot, + gridDim.x * R,
-// ..., and keeps the weight gradient of its columns in registers; the slots'
-// sums go to one partial row per block and slot.
+// ..., and keeps the weight gradient of its columns in registers; each block's
+// sums go to its partial row.
 template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16, bool VEC>
 __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel(const __grid_constant__ NormBwdArgs a) {
     using S = RowShape<W>;
@@ -259,15 +401,109 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel
             put8<DXBF16, VEC>(a.dx, row * a.ld_dx + col, valid, d);
         }
     }
-    if (a.dweight != nullptr) {
+    if (a.dweight == nullptr) return;
+    if constexpr (W == 1) {        // the block's four rows together
+        __shared__ float s_dw[S::kRows][256 * NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_dw[threadIdx.x >> 5][8 * (t + 32 * j) + e] = dw[j][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.cols; c += S::kThreads)
+            a.partial[blockIdx.x * a.cols + c] = (s_dw[0][c] + s_dw[1][c]) + (s_dw[2][c] + s_dw[3][c]);
+    } else {
+        write_partial<W, NV>(a, dw);
+    }
+}
+
+// Backward through the ring: h, dy and dh of the next rows are on their way
+// while a row's dot product is reduced.
+template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16>
+__global__ void __launch_bounds__(32 * W) rmsnorm_backward_ring_kernel(const __grid_constant__ NormBwdArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ RingState st;
+    __shared__ float s_sum[2][W];
+    const int t = threadIdx.x;
+    const int cols = static_cast<int>(a.cols);
+    const bool has_dh = a.dh != nullptr;
+    const uint32_t h_bytes = static_cast<uint32_t>(cols) * (SBF16 ? 2u : 4u);
+    const uint32_t g_bytes = static_cast<uint32_t>(cols) * (DYBF16 ? 2u : 4u);
+    const int64_t n = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    auto issue = [&](int64_t k) {
+        const int s = static_cast<int>(k % a.stages);
+        const int64_t row = blockIdx.x + k * gridDim.x;
+        uint8_t *buf = ring + s * a.stage_bytes;
+        mbar_arrive_expect_tx(&st.full[s], h_bytes + g_bytes + (has_dh ? h_bytes : 0u));
+        bulk_load(buf, static_cast<const uint8_t *>(a.h) + row * a.ld_h * (SBF16 ? 2 : 4), h_bytes, &st.full[s]);
+        bulk_load(buf + h_bytes, static_cast<const uint8_t *>(a.dy) + row * a.ld_dy * (DYBF16 ? 2 : 4), g_bytes,
+                  &st.full[s]);
+        if (has_dh)
+            bulk_load(buf + h_bytes + g_bytes, static_cast<const uint8_t *>(a.dh) + row * a.ld_dh * (SBF16 ? 2 : 4),
+                      h_bytes, &st.full[s]);
+    };
+    if (t == 0) {
+        for (int s = 0; s < a.stages; ++s) mbar_init(&st.full[s], 1);
+        st.abort = 0u;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (t == 0)
+        for (int64_t k = 0; k < a.stages && k < n; ++k) issue(k);
+    // 1024 threads have 64 registers each: they read the weight again for each
+    // row (from L1)
+    constexpr bool kHoldWeight = W < 32;
+    float w[NV][8], dw[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int col = 8 * (t + 32 * W * j);
+        if constexpr (kHoldWeight) load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, w[j]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
+    }
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    int s = 0;
+    uint32_t parity = 0;
+    bool bad = false;
+    int64_t k = 0;
+    for (; k < n; ++k) {
+        const int64_t row = blockIdx.x + k * gridDim.x;
+        const float r = a.rstd[row];
+        bad = !mbar_wait(&st.full[s], parity, kErrTimeoutTransform, &st.abort);
+        const uint8_t *buf = ring + s * a.stage_bytes;
+        float xh[NV][8], g[NV][8], d[NV][8];
+        float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = 8 * (t + S::kRowThreads * j);
+            const int col = 8 * (t + 32 * W * j);
+            load8s<SBF16>(buf, col, col < cols, xh[j]);
+            load8s<DYBF16>(buf + h_bytes, col, col < cols, g[j]);
+            load8s<SBF16>(buf + h_bytes + g_bytes, col, has_dh && col < cols, d[j]);
+            if constexpr (!kHoldWeight) load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, w[j]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (col + e < a.cols) a.partial[slot * a.cols + col + e] = dw[j][e];
+            for (int e = 0; e < 8; ++e) {
+                xh[j][e] *= r;
+                dw[j][e] = fmaf(g[j][e], xh[j][e], dw[j][e]);
+                g[j][e] *= w[j][e];
+                dot = fmaf(g[j][e], xh[j][e], dot);
+            }
+        }
+        dot = row_sum<W>(dot, s_sum[k & 1], &bad) * inv_cols;
+        if (bad) break;
+        if (t == 0 && k + a.stages < n) issue(k + a.stages);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = 8 * (t + 32 * W * j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[j][e] = fmaf(r, g[j][e] - xh[j][e] * dot, d[j][e]);
+            put8<DXBF16, true>(a.dx, row * a.ld_dx + col, cols - col, d[j]);
+        }
+        if (++s == a.stages) {
+            s = 0;
+            parity ^= 1u;
         }
     }
+    if (bad && t == 0) drain_ring(st, k, n < k + a.stages ? n : k + a.stages, a.stages);
+    if (a.dweight != nullptr) write_partial<W, NV>(a, dw);
 }
 
 template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8>
@@ -307,10 +543,14 @@ template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16>
 cudaError_t launch_bwd_vec(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
     using S = RowShape<W>;
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (a.vec)
-        rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, true><<<grid, S::kThreads, 0, stream>>>(a);
-    else
-        rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, false><<<grid, S::kThreads, 0, stream>>>(a);
+    // aligned rows of 1025 to 8192 elements always fit the ring
+    if constexpr (W == 1 || W > 8) {
+        if (a.vec) {
+            rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, true><<<grid, S::kThreads, 0, stream>>>(a);
+            return cudaGetLastError();
+        }
+    }
+    rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, false><<<grid, S::kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -328,19 +568,111 @@ cudaError_t launch_bwd_shape(const NormBwdArgs &a, int64_t blocks, cudaStream_t 
     }
 }
 
-// Rows per block and blocks of the backward pass (a function of the shape
-// alone): enough blocks for every SM to hold two to four.
+// Width of the rings: warps per row with two vectors per thread.
+template <typename F>
+cudaError_t with_ring_shape(int64_t width, F f) {
+    if (width <= 2048) return f(std::integral_constant<int, 4>());
+    if (width <= 4096) return f(std::integral_constant<int, 8>());
+    if (width <= 8192) return f(std::integral_constant<int, 16>());
+    return f(std::integral_constant<int, 32>());
+}
+
+// Blocks per SM: 1024 threads in all forward (at most 64 registers each), 512
+// backward (128: the weight gradient stays in registers).
+int fwd_blocks_per_sm(int64_t width) { return width <= 2048 ? 8 : width <= 4096 ? 4 : width <= 8192 ? 2 : 1; }
+int bwd_blocks_per_sm(int64_t width) { return width <= 2048 ? 4 : width <= 4096 ? 2 : 1; }
+
+constexpr int64_t kRingSmem = 216 * 1024;      // of the SM's shared memory, over its blocks
+
+// Stages of a ring whose rows take row_bytes; below 2 it is not used.
+int ring_stages(int64_t row_bytes, int blocks_per_sm) {
+    const int64_t s = kRingSmem / blocks_per_sm / ((row_bytes + 127) / 128 * 128);
+    return static_cast<int>(s < kMaxStages ? s : kMaxStages);
+}
+
+// Blocks of the backward pass (a function of the shape alone: so are the
+// workspace and the order of the sums).
 int64_t bwd_blocks(int64_t rows, int64_t cols) {
     const int64_t per = cols <= 1024 ? 4 : 1;
     const int64_t need = (rows + per - 1) / per;
-    const int64_t most = int64_t(148) * (cols <= 4096 ? 4 : cols <= 8192 ? 2 : 1);
+    const int64_t most = int64_t(148) * (cols <= 1024 ? 4 : bwd_blocks_per_sm(cols));
     return need < most ? need : most;
+}
+
+template <int W, bool SBF16, bool XBF16, bool RES, bool OUT8>
+cudaError_t launch_fwd_ring(const NormArgs &a, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    const int smem = a.stages * static_cast<int>(a.stage_bytes);
+    auto *kernel = rmsnorm_ring_kernel<W, 2, SBF16, XBF16, RES, OUT8>;
+    const cudaError_t e = allow_smem(kernel, kRingSmem, done);
+    if (e != cudaSuccess) return e;
+    const int64_t most = int64_t(148) * fwd_blocks_per_sm(a.kpad);
+    kernel<<<static_cast<unsigned>(a.rows < most ? a.rows : most), 32 * W, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int W>
+cudaError_t launch_fwd_ring_types(const NormArgs &a, cudaStream_t stream) {
+    const bool out8 = a.elems8 != nullptr;
+    if (a.residual == nullptr) {
+        if (a.x_bf16)
+            return out8 ? launch_fwd_ring<W, true, true, false, true>(a, stream)
+                        : launch_fwd_ring<W, true, true, false, false>(a, stream);
+        return out8 ? launch_fwd_ring<W, false, false, false, true>(a, stream)
+                    : launch_fwd_ring<W, false, false, false, false>(a, stream);
+    }
+    switch ((a.stream_bf16 ? 4 : 0) | (a.x_bf16 ? 2 : 0) | (out8 ? 1 : 0)) {
+        case 0: return launch_fwd_ring<W, false, false, true, false>(a, stream);
+        case 1: return launch_fwd_ring<W, false, false, true, true>(a, stream);
+        case 2: return launch_fwd_ring<W, false, true, true, false>(a, stream);
+        case 3: return launch_fwd_ring<W, false, true, true, true>(a, stream);
+        case 4: return launch_fwd_ring<W, true, false, true, false>(a, stream);
+        case 5: return launch_fwd_ring<W, true, false, true, true>(a, stream);
+        case 6: return launch_fwd_ring<W, true, true, true, false>(a, stream);
+        default: return launch_fwd_ring<W, true, true, true, true>(a, stream);
+    }
+}
+
+template <int W, bool SBF16, bool DYBF16, bool DXBF16>
+cudaError_t launch_bwd_ring(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    const int smem = a.stages * static_cast<int>(a.stage_bytes);
+    auto *kernel = rmsnorm_backward_ring_kernel<W, 2, SBF16, DYBF16, DXBF16>;
+    const cudaError_t e = allow_smem(kernel, kRingSmem, done);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(blocks), 32 * W, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int W>
+cudaError_t launch_bwd_ring_types(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
+    switch ((a.stream_bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.dx_bf16 ? 1 : 0)) {
+        case 0: return launch_bwd_ring<W, false, false, false>(a, blocks, stream);
+        case 1: return launch_bwd_ring<W, false, false, true>(a, blocks, stream);
+        case 2: return launch_bwd_ring<W, false, true, false>(a, blocks, stream);
+        case 3: return launch_bwd_ring<W, false, true, true>(a, blocks, stream);
+        case 4: return launch_bwd_ring<W, true, false, false>(a, blocks, stream);
+        case 5: return launch_bwd_ring<W, true, false, true>(a, blocks, stream);
+        case 6: return launch_bwd_ring<W, true, true, false>(a, blocks, stream);
+        default: return launch_bwd_ring<W, true, true, true>(a, blocks, stream);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_rmsnorm(const NormArgs &a, cudaStream_t stream) {
-    const int64_t width = a.elems8 != nullptr ? a.kpad : a.cols;
+// Rows of more than 1024 elements that bulk copies can fetch (vec: 16-byte
+// aligned rows) go through the ring once a block gets more than one of them;
+// short rows have a warp each, and few, odd or very long rows a block each.
+cudaError_t launch_rmsnorm(const NormArgs &args, cudaStream_t stream) {
+    NormArgs a = args;
+    const int64_t width = a.kpad;
+    if (a.vec && width > 1024 && width <= 16384 && a.rows > int64_t(148) * fwd_blocks_per_sm(width)) {
+        const int64_t bytes = a.cols * ((a.x_bf16 ? 2 : 4) + (a.residual == nullptr ? 0 : a.stream_bf16 ? 2 : 4));
+        a.stages = ring_stages(bytes, fwd_blocks_per_sm(width));
+        a.stage_bytes = (bytes + 127) / 128 * 128;
+        if (a.stages >= 2)
+            return with_ring_shape(width, [&](auto w) { return launch_fwd_ring_types<decltype(w)::value>(a, stream); });
+    }
     if (width <= 256) return launch_fwd_shape<1, 1>(a, stream);
     if (width <= 1024) return launch_fwd_shape<1, 4>(a, stream);
     if (width <= 4096) return launch_fwd_shape<4, 4>(a, stream);
@@ -349,14 +681,23 @@ cudaError_t launch_rmsnorm(const NormArgs &a, cudaStream_t stream) {
     return launch_fwd_shape<32, 4>(a, stream);
 }
 
-int64_t rmsnorm_backward_slots(int64_t rows, int64_t cols) {
-    return rows <= 0 ? 0 : bwd_blocks(rows, cols) * (cols <= 1024 ? 4 : 1);
-}
+int64_t rmsnorm_backward_slots(int64_t rows, int64_t cols) { return rows <= 0 ? 0 : bwd_blocks(rows, cols); }
 
-cudaError_t launch_rmsnorm_backward(const NormBwdArgs &a, cudaStream_t stream) {
+cudaError_t launch_rmsnorm_backward(const NormBwdArgs &args, cudaStream_t stream) {
+    NormBwdArgs a = args;
     const int64_t blocks = bwd_blocks(a.rows, a.cols);
-    cudaError_t e;
-    if (a.cols <= 256)
+    cudaError_t e = cudaErrorInvalidValue;
+    bool ring = false;
+    if (a.vec && a.cols > 1024 && a.cols <= 16384) {
+        const int64_t st = a.stream_bf16 ? 2 : 4;
+        const int64_t bytes = a.cols * ((a.dh == nullptr ? st : 2 * st) + (a.dy_bf16 ? 2 : 4));
+        a.stages = ring_stages(bytes, bwd_blocks_per_sm(a.cols));
+        a.stage_bytes = (bytes + 127) / 128 * 128;
+        ring = a.stages >= 2;
+    }
+    if (ring)
+        e = with_ring_shape(a.cols, [&](auto w) { return launch_bwd_ring_types<decltype(w)::value>(a, blocks, stream); });
+    else if (a.cols <= 256)
         e = launch_bwd_shape<1, 1>(a, blocks, stream);
     else if (a.cols <= 1024)
         e = launch_bwd_shape<1, 4>(a, blocks, stream);
@@ -369,7 +710,15 @@ cudaError_t launch_rmsnorm_backward(const NormBwdArgs &a, cudaStream_t stream) {
     else
         e = launch_bwd_shape<32, 4>(a, blocks, stream);
     if (e != cudaSuccess || a.dweight == nullptr) return e;
-    return launch_column_sums(a.partial, rmsnorm_backward_slots(a.rows, a.cols), a.cols, a.dweight, stream);
+    return launch_column_sums(a.partial, blocks, a.cols, a.dweight, stream);
+}
+
+// Host side of ufp4_check_device_status for this translation unit's waits.
+cudaError_t norm_read_and_clear_error_word(uint32_t *out) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_error_word, sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    const uint32_t zero = 0;
+    return cudaMemcpyToSymbol(g_error_word, &zero, sizeof(uint32_t));
 }
 
 }  // namespace ufp4

@@ -125,6 +125,7 @@ struct EpiArgs {
     int64_t ld_res, ld_pre, ld_out;
     int32_t bias_bf16, res_bf16, pre_bf16, out_bf16;   // else fp32
     int32_t vec_bias, vec_res, vec_pre, vec_out;
+    int32_t vec_all;         // all of those that are present
     int32_t act;             // ufp4_act_t
 };
 
@@ -217,8 +218,10 @@ struct NormArgs {
     void *y;                              // bf16 output, or nullptr
     uint8_t *elems8, *scales, *sf_atoms;  // 8-bit output, or nullptr (atoms optional)
     float *rstd;                          // [rows] or nullptr
-    int64_t rows, cols, kpad;             // kpad: elements per row of the 8-bit output
+    int64_t rows, cols, kpad;             // kpad: elements per row of the 8-bit output (else cols)
     int64_t ld_x, ld_res, ld_h, ld_y, scale_ld, atoms_k;
+    int64_t stage_bytes;                  // ring of rows in shared memory (filled by the launcher)
+    int32_t stages;
     float eps;
     int32_t x_bf16, stream_bf16, weight_bf16, vec, vec_weight;
 };
@@ -231,6 +234,8 @@ struct NormBwdArgs {
     float *dweight;                       // or nullptr
     float *partial;                       // [slots][cols] when dweight
     int64_t rows, cols, ld_dy, ld_h, ld_dh, ld_dx;
+    int64_t stage_bytes;                  // as above
+    int32_t stages;
     int32_t dy_bf16, stream_bf16, dx_bf16, weight_bf16, vec, vec_weight;
 };
 int64_t rmsnorm_backward_slots(int64_t rows, int64_t cols);

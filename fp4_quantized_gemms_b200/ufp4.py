@@ -543,20 +543,35 @@ def _dtype(t: torch.Tensor, name: str) -> int:
 
 def _pitch(t: torch.Tensor, rows: int, cols: int, name: str) -> int:
     """Row pitch of a [rows, cols] tensor with contiguous rows."""
-    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols, f"{name}: shape {(rows, cols)}, got {tuple(t.shape)}")
-    _need(cols <= 1 or t.stride(1) == 1, f"{name}: rows have to be contiguous")
-    return t.stride(0) if rows > 1 else max(cols, 1)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: shape {(rows, cols)}, got {tuple(t.shape)}")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}: rows have to be contiguous")
+    return pitch if rows > 1 else max(cols, 1)
 
 
 def _vector(t: torch.Tensor, n: int, name: str):
-    _need(t.dim() == 1 and t.shape[0] == n and (n <= 1 or t.stride(0) == 1),
-          f"{name}: a contiguous vector of {n}, got {tuple(t.shape)}")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: a contiguous vector of {n}, got {tuple(t.shape)}")
 
 
-def _same_device(device: torch.device, *tensors):
+def _device(*tensors) -> torch.device:
+    """The CUDA device that all tensors (None skipped) are on; the first is one."""
+    device = tensors[0].device
+    if device.type != "cuda":
+        raise RuntimeError("ufp4 kernels need CUDA tensors (there is no CPU path)")
     for t in tensors:
         if t is not None and t.device != device:
+            _require_cuda(t)
             raise ValueError(f"tensors on {device} and {t.device}: one call works on one device")
+    return device
+
+
+# The current stream's handle without a Stream object (0.1 instead of 2 us a
+# call) where this torch has the accessor.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(name: str, device: torch.device, *args):
@@ -564,11 +579,12 @@ def _call(name: str, device: torch.device, *args):
     not be) on that device's current stream."""
     fn = getattr(lib(), name)
     if torch.cuda.current_device() == device.index:
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        status = fn(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(status, name)
+            status = fn(*args, _raw_stream(device.index))
+    if status != OK:
+        raise UFP4Error(status, name)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -582,12 +598,10 @@ def gemm_epilogue(a: QTensor, b: QTensor, bias: torch.Tensor | None = None, act:
     of the three GEMMs.  bias [N], residual and pre [M, N]: bfloat16 or
     float32.  pre receives A B^T + bias (what epilogue_backward needs).
     out may be the residual itself; out_dtype applies when out is None."""
-    device = a.scales.device
-    _require_cuda(a.scales, b.scales, bias, residual, out, pre)
-    _same_device(device, b.scales, bias, residual, out, pre)
+    device = _device(a.scales, b.scales, bias, residual, out, pre)
     m, n = a.rows, b.rows
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=device)
+        out = a.scales.new_empty((m, n), dtype=out_dtype)
     od, ldo = _dtype(out, "out"), _pitch(out, m, n, "out")
     e = EpilogueC(act=act)
     if bias is not None:
@@ -608,9 +622,7 @@ def epilogue_backward(dout: torch.Tensor, pre: torch.Tensor | None, act: int, dp
     """(dpre, dbias) of gemm_epilogue: dpre = dout * act'(pre) (bfloat16 unless
     a tensor is given), dbias its column sums (float32, or None).  pre may be
     None for ACT_NONE."""
-    _require_cuda(dout, pre, dpre)
-    device = dout.device
-    _same_device(device, pre, dpre)
+    device = _device(dout, pre, dpre)
     _need(dout.dim() == 2, "dout: a matrix")
     m, n = dout.shape
     gd, ldg = _dtype(dout, "dout"), _pitch(dout, m, n, "dout")
@@ -620,12 +632,12 @@ def epilogue_backward(dout: torch.Tensor, pre: torch.Tensor | None, act: int, dp
     else:
         _need(act == ACT_NONE, "pre: needed for an activation")
     if dpre is None:
-        dpre = torch.empty((m, n), dtype=torch.bfloat16, device=device)
+        dpre = dout.new_empty((m, n), dtype=torch.bfloat16)
     dd, ldd = _dtype(dpre, "dpre"), _pitch(dpre, m, n, "dpre")
     dbias = work = None
     if want_dbias:
-        dbias = torch.empty(n, dtype=torch.float32, device=device)
-        work = torch.empty(lib().ufp4_epilogue_backward_workspace(m, n), dtype=torch.uint8, device=device)
+        dbias = dout.new_empty(n, dtype=torch.float32)
+        work = dout.new_empty(lib().ufp4_epilogue_backward_workspace(m, n), dtype=torch.uint8)
     _call("ufp4_epilogue_backward", device, dout.data_ptr(), ldg, gd, _ptr(pre), ldz, zd, act, m, n,
           dpre.data_ptr(), ldd, dd, _ptr(dbias), _ptr(work))
     return dpre, dbias
@@ -644,9 +656,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None
     an 8-bit GEMM operand (empty_qtensor(rows, cols, CFG_8BIT)).  h is x when
     there is no residual; h may be the residual itself (or x) to update the
     stream in place.  rstd [rows] float32 is what rmsnorm_backward needs."""
-    _require_cuda(x, weight, residual, y, h, rstd, q.scales if q is not None else None)
-    device = x.device
-    _same_device(device, weight, residual, y, h, rstd, q.scales if q is not None else None)
+    device = _device(x, weight, residual, y, h, rstd, q.scales if q is not None else None)
     _need(x.dim() == 2, "x: a matrix")
     rows, cols = x.shape
     xd, ldx = _dtype(x, "x"), _pitch(x, rows, cols, "x")
@@ -657,18 +667,18 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None
     if residual is not None:
         sd, ldr = _dtype(residual, "residual"), _pitch(residual, rows, cols, "residual")
         if h is None:
-            h = torch.empty((rows, cols), dtype=residual.dtype, device=device)
+            h = residual.new_empty((rows, cols))
         _need(h.dtype == residual.dtype, "h: the residual's type")
         ldh = _pitch(h, rows, cols, "h")
     else:
         _need(h is None, "h: x itself without a residual")
     if q is None:
         if y is None:
-            y = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+            y = x.new_empty((rows, cols), dtype=torch.bfloat16)
         _need(y.dtype == torch.bfloat16, "y: bfloat16")
         ldy = _pitch(y, rows, cols, "y")
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+        rstd = x.new_empty(rows, dtype=torch.float32)
     _need(rstd.dtype == torch.float32, "rstd: float32")
     _vector(rstd, rows, "rstd")
     _call("ufp4_rmsnorm", device, x.data_ptr(), ldx, xd, _ptr(residual), ldr, sd, weight.data_ptr(),
@@ -683,9 +693,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     """(dx, dweight) of rmsnorm: dx is the gradient of x and of the residual
     (the stream's type unless a tensor is given), with dh, the gradient that
     arrives at h itself, added in; dweight float32 (or None)."""
-    _require_cuda(dy, h, weight, rstd, dh, dx)
-    device = h.device
-    _same_device(device, dy, weight, rstd, dh, dx)
+    device = _device(h, dy, weight, rstd, dh, dx)
     _need(h.dim() == 2, "h: a matrix")
     rows, cols = h.shape
     sd, ldh = _dtype(h, "h"), _pitch(h, rows, cols, "h")
@@ -698,12 +706,12 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
         _need(dh.dtype == h.dtype, "dh: the stream's type")
         lddh = _pitch(dh, rows, cols, "dh")
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=h.dtype, device=device)
+        dx = h.new_empty((rows, cols))
     dd, lddx = _dtype(dx, "dx"), _pitch(dx, rows, cols, "dx")
     dweight = work = None
     if want_dweight:
-        dweight = torch.empty(cols, dtype=torch.float32, device=device)
-        work = torch.empty(lib().ufp4_rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=device)
+        dweight = h.new_empty(cols, dtype=torch.float32)
+        work = h.new_empty(lib().ufp4_rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8)
     _call("ufp4_rmsnorm_backward", device, dy.data_ptr(), ldg, gd, h.data_ptr(), ldh, sd, weight.data_ptr(),
           _dtype(weight, "weight"), rstd.data_ptr(), _ptr(dh), lddh, rows, cols, dx.data_ptr(), lddx, dd,
           _ptr(dweight), _ptr(work))
@@ -723,19 +731,17 @@ def moe_balance(logits: torch.Tensor, experts: torch.Tensor, coef: float = 1.0, 
     tokens [1] int64).  logits [tokens, E] bfloat16 or float32; experts
     [tokens, k] int32, the chosen experts (an index outside [0, E) is a
     dropped choice); mask [tokens], False for tokens that do not count."""
-    _require_cuda(logits, experts, mask)
-    device = logits.device
-    _same_device(device, experts, mask)
+    device = _device(logits, experts, mask)
     _need(logits.dim() == 2, "logits: a matrix")
     tokens, n = logits.shape
     dt, ld = _dtype(logits, "logits"), _pitch(logits, tokens, n, "logits")
     _need(experts.dtype == torch.int32 and experts.dim() == 2 and experts.shape[0] == tokens and
           experts.is_contiguous(), "experts: a contiguous int32 matrix, a row per token")
     mp = _mask_ptr(mask, tokens)
-    loss = torch.empty(1, dtype=torch.float32, device=device)
-    counts = torch.empty(n, dtype=torch.int64, device=device)
-    valid = torch.empty(1, dtype=torch.int64, device=device)
-    work = torch.empty(lib().ufp4_moe_balance_workspace(n), dtype=torch.uint8, device=device)
+    loss = logits.new_empty(1, dtype=torch.float32)
+    counts = logits.new_empty(n, dtype=torch.int64)
+    valid = logits.new_empty(1, dtype=torch.int64)
+    work = logits.new_empty(lib().ufp4_moe_balance_workspace(n), dtype=torch.uint8)
     _call("ufp4_moe_balance", device, logits.data_ptr(), ld, dt, tokens, n, experts.data_ptr(), experts.shape[1], mp,
           coef, loss.data_ptr(), counts.data_ptr(), valid.data_ptr(), work.data_ptr())
     return loss, counts, valid
@@ -747,9 +753,7 @@ def moe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: tor
     """Gradient of moe_balance's loss with respect to the logits.  counts and
     tokens (the number that count) are moe_balance's results, topk the
     choices per token, dloss [1] float32 the loss's own gradient."""
-    _require_cuda(logits, counts, tokens, dloss, mask, dlogits)
-    device = logits.device
-    _same_device(device, counts, tokens, dloss, mask, dlogits)
+    device = _device(logits, counts, tokens, dloss, mask, dlogits)
     _need(logits.dim() == 2, "logits: a matrix")
     rows, n = logits.shape
     dt, ld = _dtype(logits, "logits"), _pitch(logits, rows, n, "logits")
@@ -757,7 +761,7 @@ def moe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: tor
     _vector(counts, n, "counts")
     _need(dloss.dtype == torch.float32 and dloss.numel() == 1, "dloss: one float32")
     if dlogits is None:
-        dlogits = torch.empty((rows, n), dtype=logits.dtype, device=device)
+        dlogits = logits.new_empty((rows, n))
     _need(dlogits.dtype == logits.dtype, "dlogits: the logits' type")
     ldd = _pitch(dlogits, rows, n, "dlogits")
     _call("ufp4_moe_balance_backward", device, logits.data_ptr(), ld, dt, rows, n, topk, _mask_ptr(mask, rows), coef,
@@ -771,11 +775,9 @@ def _tensor_table(grads, out):
     for i, t in enumerate(grads):
         o = t if out is None else out[i]
         if device is None:
-            device = t.device
-        if not (t.is_cuda and o.is_cuda):
-            raise RuntimeError("ufp4 kernels need CUDA tensors (there is no CPU path)")
+            device = _device(t)
         if t.device != device or o.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}: one call works on one device")
+            _device(grads[0], t, o)
         if not (t.is_contiguous() and o.is_contiguous()) or t.numel() != o.numel():
             raise ValueError(f"gradient {i}: contiguous tensors, a destination of the same size")
         table.extend((t.data_ptr(), o.data_ptr(), t.numel(), _dtype(t, "gradient") | _dtype(o, "out") << 32))

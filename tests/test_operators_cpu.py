@@ -176,7 +176,7 @@ def test_rmsnorm_backward(L):
     assert call(rows=-1) == BAD and call(cols=40000, ldg=40000, ldh=40000, lddh=40000, lddx=40000) == UNSUP
     assert call(cols=0) == OK and call(rows=0, dw=None) == OK
     W = L.ufp4_rmsnorm_backward_workspace
-    assert W(0, 64) == 0 and W(5, 0) == 0 and W(1, 2048) == 2048 * 4 and W(1, 64) == 4 * 64 * 4
+    assert W(0, 64) == 0 and W(5, 0) == 0 and W(1, 2048) == 2048 * 4 and W(1, 64) == 64 * 4
 
 
 def test_moe_balance(L):
