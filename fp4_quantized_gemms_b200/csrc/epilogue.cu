@@ -30,32 +30,6 @@ constexpr int kBwdWarps = kBwdThreads / 32;
 constexpr int kBwdCols = 256;      // columns of a block
 constexpr int kBwdUnroll = 4;      // rows of a warp in flight
 
-// Eight elements of a row as loaded, bf16 or fp32.
-template <bool BF16>
-struct Raw8 {
-    uint4 w[BF16 ? 1 : 2];
-    __device__ __forceinline__ void load(const void *p, int64_t i) {
-        const uint4 *q = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i)
-                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
-        w[0] = __ldcs(q);
-        if constexpr (!BF16) w[1] = __ldcs(q + 1);
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        if constexpr (BF16) {
-            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = bf16_lo(u[j]);
-                v[2 * j + 1] = bf16_hi(u[j]);
-            }
-        } else {
-            const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(u[j]);
-        }
-    }
-};
-
 template <bool BF16>
 __device__ __forceinline__ void store8(void *p, int64_t i, const float (&v)[8]) {
     if constexpr (BF16) {

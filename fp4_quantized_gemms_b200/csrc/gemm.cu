@@ -1383,8 +1383,7 @@ struct ResidualRows {
 // for each piece, and an earlier form with the choice inside and everything
 // unrolled spent its time fetching instructions (one 256 x 512 x 512 MX product
 // with GELU, bias and residual: 41 us, now 26).  The residual of the next four
-// rows is on its way while four
-// rows are finished.
+// rows is on its way while four rows are finished.
 template <int ACT>
 __device__ __forceinline__ void finish_piece(const EpiArgs &e, const uint8_t *buf, int lane, int64_t m0, int64_t m,
                                              int64_t gcol) {

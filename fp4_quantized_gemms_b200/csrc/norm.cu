@@ -416,6 +416,94 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel
     }
 }
 
+// Backward of short aligned rows: a warp takes U rows at a time (U NV <= 4
+// vectors of each tensor in flight per lane), all loads before the dot
+// product, the elements kept as loaded so that 16 warps fit an SM; the weight
+// is read again for each row (from L1).
+template <int NV, int U, bool SBF16, bool DYBF16, bool DXBF16>
+__global__ void __launch_bounds__(128, 4) rmsnorm_backward_short_kernel(const __grid_constant__ NormBwdArgs a) {
+    __shared__ float s_dw[4][256 * NV];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cols = static_cast<int>(a.cols);
+    const bool has_dh = a.dh != nullptr;
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    float dw[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * U;
+    for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * 4 + warp) * U; row0 < a.rows; row0 += step) {
+        Raw8<SBF16> h[U][NV], d[U][NV];
+        Raw8<DYBF16> g[U][NV];
+        float r[U], dot[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u;
+            const bool in = row < a.rows;
+            r[u] = in ? a.rstd[row] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = 8 * (lane + 32 * j);
+                h[u][j].zero();
+                g[u][j].zero();
+                d[u][j].zero();
+                if (in && col < cols) {
+                    h[u][j].load(a.h, row * a.ld_h + col);
+                    g[u][j].load(a.dy, row * a.ld_dy + col);
+                    if (has_dh) d[u][j].load(a.dh, row * a.ld_dh + col);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) dot[u] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = 8 * (lane + 32 * j);
+            float w[8];
+            load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, w);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[8], y[8];
+                h[u][j].get(x);
+                g[u][j].get(y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] *= r[u];
+                    dw[j][e] = fmaf(y[e], x[e], dw[j][e]);
+                    dot[u] = fmaf(y[e] * w[e], x[e], dot[u]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) dot[u] = warp_sum(dot[u]) * inv_cols;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = 8 * (lane + 32 * j);
+            float w[8];
+            load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, w);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[8], y[8], o[8];
+                h[u][j].get(x);
+                g[u][j].get(y);
+                d[u][j].get(o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = fmaf(r[u], y[e] * w[e] - x[e] * r[u] * dot[u], o[e]);
+                if (row0 + u < a.rows) put8<DXBF16, true>(a.dx, (row0 + u) * a.ld_dx + col, cols - col, o);
+            }
+        }
+    }
+    if (a.dweight == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_dw[warp][8 * (lane + 32 * j) + e] = dw[j][e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += 128)
+        a.partial[blockIdx.x * a.cols + c] = (s_dw[0][c] + s_dw[1][c]) + (s_dw[2][c] + s_dw[3][c]);
+}
+
 // Backward through the ring: h, dy and dh of the next rows are on their way
 // while a row's dot product is reduced.
 template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16>
@@ -543,14 +631,31 @@ template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16>
 cudaError_t launch_bwd_vec(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
     using S = RowShape<W>;
     const unsigned grid = static_cast<unsigned>(blocks);
-    // aligned rows of 1025 to 8192 elements always fit the ring
-    if constexpr (W == 1 || W > 8) {
+    // aligned rows of up to 1024 elements have their own kernel, and those of
+    // 1025 to 8192 always fit the ring
+    if constexpr (W > 8) {
         if (a.vec) {
             rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, true><<<grid, S::kThreads, 0, stream>>>(a);
             return cudaGetLastError();
         }
     }
     rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, false><<<grid, S::kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int NV, int U>
+cudaError_t launch_bwd_short(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
+    const unsigned n = static_cast<unsigned>(blocks);
+    switch ((a.stream_bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.dx_bf16 ? 1 : 0)) {
+        case 0: rmsnorm_backward_short_kernel<NV, U, false, false, false><<<n, 128, 0, stream>>>(a); break;
+        case 1: rmsnorm_backward_short_kernel<NV, U, false, false, true><<<n, 128, 0, stream>>>(a); break;
+        case 2: rmsnorm_backward_short_kernel<NV, U, false, true, false><<<n, 128, 0, stream>>>(a); break;
+        case 3: rmsnorm_backward_short_kernel<NV, U, false, true, true><<<n, 128, 0, stream>>>(a); break;
+        case 4: rmsnorm_backward_short_kernel<NV, U, true, false, false><<<n, 128, 0, stream>>>(a); break;
+        case 5: rmsnorm_backward_short_kernel<NV, U, true, false, true><<<n, 128, 0, stream>>>(a); break;
+        case 6: rmsnorm_backward_short_kernel<NV, U, true, true, false><<<n, 128, 0, stream>>>(a); break;
+        default: rmsnorm_backward_short_kernel<NV, U, true, true, true><<<n, 128, 0, stream>>>(a); break;
+    }
     return cudaGetLastError();
 }
 
@@ -697,8 +802,10 @@ cudaError_t launch_rmsnorm_backward(const NormBwdArgs &args, cudaStream_t stream
     }
     if (ring)
         e = with_ring_shape(a.cols, [&](auto w) { return launch_bwd_ring_types<decltype(w)::value>(a, blocks, stream); });
-    else if (a.cols <= 256)
-        e = launch_bwd_shape<1, 1>(a, blocks, stream);
+    else if (a.cols <= 1024 && a.vec)
+        e = a.cols <= 256   ? launch_bwd_short<1, 4>(a, blocks, stream)
+            : a.cols <= 512 ? launch_bwd_short<2, 2>(a, blocks, stream)
+                            : launch_bwd_short<4, 1>(a, blocks, stream);
     else if (a.cols <= 1024)
         e = launch_bwd_shape<1, 4>(a, blocks, stream);
     else if (a.cols <= 4096)

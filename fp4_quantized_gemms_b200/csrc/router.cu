@@ -136,24 +136,39 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const __grid_
     if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = s_tokens;
 }
 
-// One block: adds the partial rows, writes counts, the token count and the loss.
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_constant__ BalanceArgs a, int blocks) {
+// One block: adds the partial rows, writes counts, the token count and the
+// loss.  `width` (a power of two, at least the experts) threads side by side
+// take the experts and 1024 / width slices every so-many-th row each; the
+// slices are added in order.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_constant__ BalanceArgs a, int blocks, int width) {
+    __shared__ float s_prob[1024];
+    __shared__ int64_t s_count[1024];
     __shared__ double s_red[32];
     __shared__ int64_t s_tok[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = threadIdx.x & (width - 1), slice = threadIdx.x / width, slices = 1024 / width;
     int64_t tok = 0;
     for (int b = threadIdx.x; b < blocks; b += 1024) tok += a.part_tokens[b];
-    double dot = 0.0;       // sum over this thread's experts of c_e * sum p_e
-    for (int e = threadIdx.x; e < a.experts; e += 1024) {
-        float s = 0.0f;
-        int64_t c = 0;
+    float s = 0.0f;
+    int64_t c = 0;
+    if (e < a.experts) {
 #pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
+        for (int b = slice; b < blocks; b += slices) {
             s += a.part_prob[static_cast<int64_t>(b) * a.experts + e];
             c += a.part_count[static_cast<int64_t>(b) * a.experts + e];
         }
+    }
+    s_prob[threadIdx.x] = s;
+    s_count[threadIdx.x] = c;
+    __syncthreads();
+    double dot = 0.0;       // c_e * sum of p_e
+    if (slice == 0 && e < a.experts) {
+        for (int k = 1; k < slices; ++k) {
+            s += s_prob[k * width + e];
+            c += s_count[k * width + e];
+        }
         a.counts[e] = c;
-        dot += static_cast<double>(c) * static_cast<double>(s);
+        dot = static_cast<double>(c) * static_cast<double>(s);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -239,7 +254,9 @@ cudaError_t launch_shape(const BalanceArgs &a, bool backward, cudaStream_t strea
     balance_partial_kernel<G, J, V, BF16><<<blocks, kThreads, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    balance_finish_kernel<<<1, 1024, 0, stream>>>(a, blocks);
+    int width = 1;
+    while (width < a.experts) width *= 2;
+    balance_finish_kernel<<<1, 1024, 0, stream>>>(a, blocks, width);
     return cudaGetLastError();
 }
 

@@ -63,26 +63,78 @@ __device__ __forceinline__ void store_quad(void *p, int64_t i, bool bf16, bool v
         if (e < valid) store_elem(p, i + e, bf16, e4[e]);
 }
 
+// Eight elements of a row as loaded, bf16 or fp32 (16-byte aligned, read once:
+// evict first).
+template <bool BF16>
+struct Raw8 {
+    uint4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const uint4 *q = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i)
+                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
+        w[0] = __ldcs(q);
+        if constexpr (!BF16) w[1] = __ldcs(q + 1);
+    }
+    __device__ __forceinline__ void zero() {
+        w[0] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (!BF16) w[1] = w[0];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (BF16) {
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = bf16_lo(u[j]);
+                v[2 * j + 1] = bf16_hi(u[j]);
+            }
+        } else {
+            const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(u[j]);
+        }
+    }
+};
+
 // ---------------------------------------------------------------------------
-// Activations (ufp4_act_t).  exp is the hardware's ex2 through __expf: its
-// relative error (about 2^-22 plus 2^-24 per unit of the argument) scales a
-// term that is small whenever the argument is large, so every value below is
-// within a few 1e-7 of max(|z|, 1).
+// Activations (ufp4_act_t) on the hardware's ex2 and reciprocal (ex2.approx and
+// rcp.approx: 2^-22 and 1 ulp).  The argument's own rounding adds 2^-24 per
+// unit of it to a term that is small whenever the argument is large, so every
+// value below is within a few 1e-7 of max(|z|, 1).
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// z within [-m, m]; NaN stays NaN.
+__device__ __forceinline__ float clamp_nan(float z, float m) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(-m));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(m));
+    return y;
+}
 
 // GELU in its tanh form, z (1 + tanh u) / 2 = z / (1 + exp(-2u)),
-// u = sqrt(2 / pi) (z + 0.044715 z^3).
-constexpr float kGeluA = 0.79788456080286536f;   // sqrt(2 / pi)
-constexpr float kGeluB = 0.044715f;
+// u = sqrt(2 / pi) (z + 0.044715 z^3); exp(-2u) = 2^(-z (A + B z^2)).
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGelu2A = 2.0f * 0.79788456080286536f;          // 2 sqrt(2 / pi)
+constexpr float kGelu2B = kGelu2A * 0.044715f;
 
 __device__ __forceinline__ float act_value(float z, int act) {
     switch (act) {
         case UFP4_ACT_RELU: return z < 0.0f ? 0.0f : z;          // NaN stays NaN
         case UFP4_ACT_GELU: {
-            const float u2 = 2.0f * kGeluA * z * (1.0f + kGeluB * z * z);
-            return __fdividef(z, 1.0f + __expf(-u2));
+            const float p = fmaf(-kGelu2B * kLog2e, z * z, -kGelu2A * kLog2e);
+            return z * rcp_approx(1.0f + ex2_approx(z * p));
         }
         case UFP4_ACT_GELU_ERF: return 0.5f * z * (1.0f + erff(0.70710678118654752f * z));
-        case UFP4_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+        case UFP4_ACT_SILU: return z * rcp_approx(1.0f + ex2_approx(-kLog2e * z));
         default: return z;
     }
 }
@@ -92,32 +144,30 @@ __device__ __forceinline__ float4 act_quad(float4 z, int act) {
     return make_float4(act_value(z.x, act), act_value(z.y, act), act_value(z.z, act), act_value(z.w, act));
 }
 
-// Derivative of the activation.  The GELUs and SiLU saturate: beyond |z| = 12
-// (GELU) the derivative is 0 or 1 to fp32, and the clamp keeps the products
-// of a vanishing and a growing factor finite.
+// Derivative of the activation.  With t = exp(-2u) (GELU) or exp(-z) (SiLU)
+// and s = 1 / (1 + t): d = s + z u2' s (t s), where t s = 1 - s without
+// cancellation and u2' = d(2u)/dz.  Beyond |z| = 9 (GELU) or 60 (SiLU) the
+// derivative is 0 or 1 to fp32; the clamp keeps t finite and every product in
+// range.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == UFP4_ACT_RELU) {
         return z > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (ACT == UFP4_ACT_GELU) {
-        const float c = fminf(fmaxf(z, -12.0f), 12.0f);
+        const float c = clamp_nan(z, 9.0f);
         const float c2 = c * c;
-        const float u2 = 2.0f * kGeluA * c * (1.0f + kGeluB * c2);
-        const float t = __expf(fminf(-u2, 80.0f));
-        const float sg = __fdividef(1.0f, 1.0f + t);
-        const float d = sg + c * sg * (t * sg) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * c2);
-        return z == z ? d : z;
+        const float t = ex2_approx(c * fmaf(-kGelu2B * kLog2e, c2, -kGelu2A * kLog2e));
+        const float s = rcp_approx(1.0f + t);
+        return fmaf(c * fmaf(3.0f * kGelu2B, c2, kGelu2A), t * (s * s), s);
     } else if constexpr (ACT == UFP4_ACT_GELU_ERF) {
-        const float c = fminf(fmaxf(z, -12.0f), 12.0f);
-        const float d = 0.5f * (1.0f + erff(0.70710678118654752f * c)) +
-                        c * 0.39894228040143268f * __expf(-0.5f * c * c);
-        return z == z ? d : z;
+        const float c = clamp_nan(z, 9.0f);
+        return fmaf(c * 0.39894228040143268f, ex2_approx(-0.5f * kLog2e * c * c),
+                    0.5f * (1.0f + erff(0.70710678118654752f * c)));
     } else if constexpr (ACT == UFP4_ACT_SILU) {
-        const float c = fminf(fmaxf(z, -80.0f), 80.0f);
-        const float t = __expf(-c);
-        const float sg = __fdividef(1.0f, 1.0f + t);
-        const float d = sg + c * sg * (t * sg);
-        return z == z ? d : z;
+        const float c = clamp_nan(z, 60.0f);
+        const float t = ex2_approx(-kLog2e * c);
+        const float s = rcp_approx(1.0f + t);
+        return fmaf(c, t * (s * s), s);
     } else {
         return 1.0f;
     }
