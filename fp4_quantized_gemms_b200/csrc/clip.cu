@@ -108,6 +108,7 @@ __device__ __forceinline__ int tensor_of(const ClipTable<MAX> &t, int64_t chunk)
 
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) square_sums_kernel(const __grid_constant__ ClipTable<MAX> t, double *sums) {
+    let_next_kernel_launch();
     double acc = 0.0;
     for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const ClipEntry &e = t.e[tensor_of(t, c)];
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(kThreads) square_sums_kernel(const __grid_cons
 }
 
 __device__ __forceinline__ double total_norm(const double *sums, int64_t count) {
+    wait_for_previous_kernel();
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < count; i += kThreads) s += sums[i];
     return sqrt(block_sum(s));
@@ -205,15 +207,13 @@ cudaError_t run(const ufp4_tensor_t *tensors, int32_t n, double *sums, bool scal
         count += b;
     }
     if (!scale || count == 0) {
-        norm_only_kernel<<<1, kThreads, 0, stream>>>(sums, count, norm);
-        return cudaGetLastError();
+        return launch_early(norm_only_kernel, dim3(1), dim3(kThreads), stream, sums, count, norm);
     }
     for (int32_t i = 0; i < n;) {
         i += fill(tensors, i, n, &t);
         if (t.chunks == 0) continue;
-        scale_kernel<MAX><<<static_cast<unsigned>(blocks_of(t.chunks)), kThreads, 0, stream>>>(t, sums, count, max_norm,
-                                                                                              norm);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_early(scale_kernel<MAX>, dim3(static_cast<unsigned>(blocks_of(t.chunks))),
+                                           dim3(kThreads), stream, t, sums, count, max_norm, norm);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -62,6 +62,7 @@ __device__ __forceinline__ void store_partial(const EpiBwdArgs &a, const float (
 
 template <int ACT, bool DOUT_BF16, bool PRE_BF16, bool DPRE_BF16>
 __global__ void __launch_bounds__(kBwdThreads) epilogue_backward_kernel(const __grid_constant__ EpiBwdArgs a) {
+    let_next_kernel_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kBwdCols;
     const int64_t col = col0 + 8 * lane;
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kBwdThreads) epilogue_backward_kernel(const __
 // lanes side by side.
 template <int ACT>
 __global__ void __launch_bounds__(kBwdThreads) epilogue_backward_any_kernel(const __grid_constant__ EpiBwdArgs a) {
+    let_next_kernel_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kBwdCols;
     const int64_t r_first = blockIdx.y * a.rows_per_chunk + warp;
@@ -135,26 +137,29 @@ __global__ void __launch_bounds__(kBwdThreads) epilogue_backward_any_kernel(cons
     if (a.dbias != nullptr) store_partial<false>(a, sum, col0);
 }
 
-// out[c] = sum of the partial rows: 32 columns per block, eight warps take
-// every eighth row, then the eight sums in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float *partial, int64_t rows, int64_t cols,
-                                                          float *out) {
-    __shared__ float s_sum[8][32];
+// out[c] = sum of the partial rows: 32 columns per block, its 32 warps take
+// every 32nd row, then the 32 sums in a tree.  (With eight warps the 592 partial
+// rows of a 16384 x 2048 norm took 13 us, a fifth of that call.)
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) column_sums_kernel(const float *partial, int64_t rows, int64_t cols,
+                                                                     float *out) {
+    __shared__ float s_sum[kSumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    wait_for_previous_kernel();
     float t = 0.0f;
     if (c < cols) {
-#pragma unroll 4
-        for (int64_t r = warp; r < rows; r += 8) t += partial[r * cols + c];
+#pragma unroll 8
+        for (int64_t r = warp; r < rows; r += kSumWarps) t += partial[r * cols + c];
     }
     s_sum[warp][lane] = t;
     __syncthreads();
-    if (warp == 0 && c < cols) {
-        float s = 0.0f;
+    // warp w finishes column w
+    float s = s_sum[lane][warp];
 #pragma unroll
-        for (int w = 0; w < 8; ++w) s += s_sum[w][lane];
-        out[c] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int64_t cw = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+    if (lane == 0 && cw < cols) out[cw] = s;
 }
 
 __global__ void __launch_bounds__(256) epilogue_only_kernel(const __grid_constant__ EpiArgs e, int64_t m, int64_t n) {
@@ -223,8 +228,7 @@ cudaError_t launch_epilogue_backward(const EpiBwdArgs &args, cudaStream_t stream
 
 cudaError_t launch_column_sums(const float *partial, int64_t rows, int64_t cols, float *out, cudaStream_t stream) {
     const unsigned blocks = static_cast<unsigned>((cols + 31) / 32);
-    column_sums_kernel<<<blocks, 256, 0, stream>>>(partial, rows, cols, out);
-    return cudaGetLastError();
+    return launch_early(column_sums_kernel, dim3(blocks), dim3(32 * kSumWarps), stream, partial, rows, cols, out);
 }
 
 cudaError_t launch_epilogue_only(const EpiArgs &e, int64_t m, int64_t n, int num_sms, cudaStream_t stream) {

@@ -351,6 +351,7 @@ __device__ __forceinline__ void write_partial(const NormBwdArgs &a, const float 
 // sums go to its partial row.
 template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16, bool VEC>
 __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel(const __grid_constant__ NormBwdArgs a) {
+    let_next_kernel_launch();
     using S = RowShape<W>;
     __shared__ float s_sum[2][W];
     const int t = W == 1 ? threadIdx.x & 31 : threadIdx.x;
@@ -422,6 +423,7 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel
 // is read again for each row (from L1).
 template <int NV, int U, bool SBF16, bool DYBF16, bool DXBF16>
 __global__ void __launch_bounds__(128, 4) rmsnorm_backward_short_kernel(const __grid_constant__ NormBwdArgs a) {
+    let_next_kernel_launch();
     __shared__ float s_dw[4][256 * NV];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cols = static_cast<int>(a.cols);
@@ -508,6 +510,7 @@ __global__ void __launch_bounds__(128, 4) rmsnorm_backward_short_kernel(const __
 // while a row's dot product is reduced.
 template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16>
 __global__ void __launch_bounds__(32 * W) rmsnorm_backward_ring_kernel(const __grid_constant__ NormBwdArgs a) {
+    let_next_kernel_launch();
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RingState st;
     __shared__ float s_sum[2][W];

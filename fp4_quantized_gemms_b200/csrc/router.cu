@@ -49,38 +49,60 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// Softmax of a token's logits in registers; experts beyond E and tokens that
+// Tokens that a group of lanes works on at a time: their loads and their
+// shuffle chains overlap.
+template <int J>
+constexpr int kTokensAtOnce = J <= 8 ? 4 : 1;
+
+// Softmax of U tokens' logits in registers; experts beyond E and tokens that
 // do not count (`live` false) give 0.  -inf logits give 0; a row of nothing
 // but -inf gives 0 everywhere.  NaN stays NaN.
-template <int G, int J, int V, bool BF16>
-__device__ __forceinline__ void token_softmax(const BalanceArgs &a, int64_t token, int g, bool live, float (&p)[J]) {
-    const int64_t base = token * a.ld;
+template <int G, int J, int V, bool BF16, int U>
+__device__ __forceinline__ void token_softmax(const BalanceArgs &a, const int64_t (&token)[U], const bool (&live)[U], int g,
+                                              float (&p)[U][J]) {
 #pragma unroll
-    for (int j = 0; j < J; j += V) {
-        const int e = expert_of<G, V>(g, j);
-        if constexpr (V == 4) {
-            const float4 q = (live && e < a.experts) ? load_quad(a.logits, base + e, BF16, true, 4)
-                                                     : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
-            p[j] = q.x, p[j + 1] = q.y, p[j + 2] = q.z, p[j + 3] = q.w;
-        } else {
-            p[j] = (live && e < a.experts) ? load_elem(a.logits, base + e, BF16) : -CUDART_INF_F;
+    for (int u = 0; u < U; ++u) {
+        const int64_t base = token[u] * a.ld;
+#pragma unroll
+        for (int j = 0; j < J; j += V) {
+            const int e = expert_of<G, V>(g, j);
+            const bool in = live[u] && e < a.experts;
+            if constexpr (V == 4) {
+                const float4 q = in ? load_quad(a.logits, base + e, BF16, true, 4)
+                                    : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+                p[u][j] = q.x, p[u][j + 1] = q.y, p[u][j + 2] = q.z, p[u][j + 3] = q.w;
+            } else {
+                p[u][j] = in ? load_elem(a.logits, base + e, BF16) : -CUDART_INF_F;
+            }
         }
     }
-    float m = -CUDART_INF_F;
+    float m[U], s[U];
 #pragma unroll
-    for (int j = 0; j < J; ++j) m = fmaxf(m, p[j]);
-    m = group_max<G>(m);
-    const float shift = m == -CUDART_INF_F ? 0.0f : m;
-    float s = 0.0f;
+    for (int u = 0; u < U; ++u) {
+        m[u] = -CUDART_INF_F;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        p[j] = __expf(p[j] - shift);
-        s += p[j];
+        for (int j = 0; j < J; ++j) m[u] = fmaxf(m[u], p[u][j]);
     }
-    s = group_sum<G>(s);
-    const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
 #pragma unroll
-    for (int j = 0; j < J; ++j) p[j] *= inv;
+    for (int u = 0; u < U; ++u) m[u] = group_max<G>(m[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const float shift = m[u] == -CUDART_INF_F ? 0.0f : m[u];
+        s[u] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            p[u][j] = __expf(p[u][j] - shift);
+            s[u] += p[u][j];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] = group_sum<G>(s[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const float inv = s[u] == 0.0f ? 0.0f : __fdividef(1.0f, s[u]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) p[u][j] *= inv;
+    }
 }
 
 template <int G, int J, int V, bool BF16>
@@ -90,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const __grid_
     int32_t *s_count = reinterpret_cast<int32_t *>(s_mem);          // [E]
     float *s_prob = reinterpret_cast<float *>(s_mem + E);           // [kWarps][E]
     __shared__ int32_t s_tokens;
+    let_next_kernel_launch();
     for (int i = threadIdx.x; i < E; i += kThreads) s_count[i] = 0;
     if (threadIdx.x == 0) s_tokens = 0;
     __syncthreads();
@@ -100,21 +123,32 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[j] = 0.0f;
     int32_t mine = 0;
+    constexpr int U = kTokensAtOnce<J>;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     // whole warps go round together (the shuffles need all lanes)
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < a.tokens;
-         t0 += static_cast<int64_t>(gridDim.x) * kGroups) {
-        const int64_t t = t0 + threadIdx.x / G;
-        const bool live = t < a.tokens && (a.mask == nullptr || a.mask[t] != 0);
-        float p[J];
-        token_softmax<G, J, V, BF16>(a, t, g, live, p);
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < a.tokens; t0 += U * step) {
+        int64_t t[U];
+        bool live[U];
+        int first[U];           // this lane's first choice of each token
 #pragma unroll
-        for (int j = 0; j < J; ++j) acc[j] += p[j];
-        if (live) {
-            mine += g == 0;
-            for (int i = g; i < a.topk; i += G) {
-                const int e = a.choices[t * a.topk + i];
-                if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
-            }
+        for (int u = 0; u < U; ++u) {
+            t[u] = t0 + u * step + threadIdx.x / G;
+            live[u] = t[u] < a.tokens && (a.mask == nullptr || a.mask[t[u]] != 0);
+            first[u] = live[u] && g < a.topk ? a.choices[t[u] * a.topk + g] : -1;
+        }
+        float p[U][J];
+        token_softmax<G, J, V, BF16, U>(a, t, live, g, p);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) acc[j] += p[u][j];
+            mine += live[u] && g == 0;
+            if (first[u] >= 0 && first[u] < E) atomicAdd(&s_count[first[u]], 1);
+            if (live[u])
+                for (int i = g + G; i < a.topk; i += G) {
+                    const int e = a.choices[t[u] * a.topk + i];
+                    if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
+                }
         }
     }
     // over the warp's token groups, then (in order) over the warps
@@ -148,6 +182,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const __grid_const
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int e = threadIdx.x & (width - 1), slice = threadIdx.x / width, slices = 1024 / width;
     int64_t tok = 0;
+    wait_for_previous_kernel();
     for (int b = threadIdx.x; b < blocks; b += 1024) tok += a.part_tokens[b];
     float s = 0.0f;
     int64_t c = 0;
@@ -208,27 +243,39 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const __grid
         const int e = expert_of<G, V>(g, j);
         ge[j] = e < E ? scale * static_cast<float>(a.counts_in[e]) : 0.0f;
     }
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < a.tokens;
-         t0 += static_cast<int64_t>(gridDim.x) * kGroups) {
-        const int64_t t = t0 + threadIdx.x / G;
-        const bool in = t < a.tokens;
-        const bool live = in && (a.mask == nullptr || a.mask[t] != 0);
-        float p[J];
-        token_softmax<G, J, V, BF16>(a, t, g, live, p);
-        float dot = 0.0f;
+    constexpr int U = kTokensAtOnce<J>;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGroups; t0 < a.tokens; t0 += U * step) {
+        int64_t t[U];
+        bool live[U];
 #pragma unroll
-        for (int j = 0; j < J; ++j) dot = fmaf(p[j], ge[j], dot);
-        dot = group_sum<G>(dot);
+        for (int u = 0; u < U; ++u) {
+            t[u] = t0 + u * step + threadIdx.x / G;
+            live[u] = t[u] < a.tokens && (a.mask == nullptr || a.mask[t[u]] != 0);
+        }
+        float p[U][J], dot[U];
+        token_softmax<G, J, V, BF16, U>(a, t, live, g, p);
 #pragma unroll
-        for (int j = 0; j < J; j += V) {
-            const int e = expert_of<G, V>(g, j);
-            if (in && e < E) {
-                if constexpr (V == 4)
-                    store_quad(a.dlogits, t * a.ld_d + e, BF16, true, 4,
-                               make_float4(p[j] * (ge[j] - dot), p[j + 1] * (ge[j + 1] - dot),
-                                           p[j + 2] * (ge[j + 2] - dot), p[j + 3] * (ge[j + 3] - dot)));
-                else
-                    store_elem(a.dlogits, t * a.ld_d + e, BF16, p[j] * (ge[j] - dot));
+        for (int u = 0; u < U; ++u) {
+            dot[u] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) dot[u] = fmaf(p[u][j], ge[j], dot[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) dot[u] = group_sum<G>(dot[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < J; j += V) {
+                const int e = expert_of<G, V>(g, j);
+                if (t[u] < a.tokens && e < E) {
+                    if constexpr (V == 4)
+                        store_quad(a.dlogits, t[u] * a.ld_d + e, BF16, true, 4,
+                                   make_float4(p[u][j] * (ge[j] - dot[u]), p[u][j + 1] * (ge[j + 1] - dot[u]),
+                                               p[u][j + 2] * (ge[j + 2] - dot[u]), p[u][j + 3] * (ge[j + 3] - dot[u])));
+                    else
+                        store_elem(a.dlogits, t[u] * a.ld_d + e, BF16, p[u][j] * (ge[j] - dot[u]));
+                }
             }
         }
     }
@@ -256,8 +303,7 @@ cudaError_t launch_shape(const BalanceArgs &a, bool backward, cudaStream_t strea
     if (e != cudaSuccess) return e;
     int width = 1;
     while (width < a.experts) width *= 2;
-    balance_finish_kernel<<<1, 1024, 0, stream>>>(a, blocks, width);
-    return cudaGetLastError();
+    return launch_early(balance_finish_kernel, dim3(1), dim3(1024), stream, a, blocks, width);
 }
 
 // Experts to lanes.  Rows that allow vectors of four: the fewest lanes that

@@ -205,8 +205,8 @@ struct EpiBwdArgs {
 int64_t epilogue_backward_chunks(int64_t m, int64_t n);
 cudaError_t launch_epilogue_backward(const EpiBwdArgs &a, cudaStream_t stream);
 
-// out[c] = sum over r < rows of partial[r][c], in row order within fixed
-// groups of rows.
+// out[c] = sum over r < rows of partial[r][c], in a fixed order.  Launched
+// while the kernel before it on the stream (which fills `partial`) still runs.
 cudaError_t launch_column_sums(const float *partial, int64_t rows, int64_t cols, float *out, cudaStream_t stream);
 
 // RMS norm (norm.cu).  vec: cols % 8 == 0 and every matrix allows 16-byte
