@@ -25,7 +25,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                         // elements per thread and step
-constexpr int64_t kChunk = 16384;               // elements of a chunk: 8 steps of a block
+// Elements of a chunk: 8 steps of a block, or fewer where that leaves SMs
+// without one (300,000 elements: 22 chunks of 8 steps took 8 us a pass, 148
+// of one step 4).
+constexpr int64_t kChunkMax = 16384, kChunkMin = kVec * kThreads;
 
 // Eight elements from p[i]; `vec`: 16-byte accesses are allowed.
 __device__ __forceinline__ void get8(const void *p, int64_t i, bool bf16, bool vec, int valid, float (&v)[8]) {
@@ -112,8 +115,8 @@ __global__ void __launch_bounds__(kThreads) square_sums_kernel(const __grid_cons
     double acc = 0.0;
     for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const ClipEntry &e = t.e[tensor_of(t, c)];
-        const int64_t first = (c - e.chunk0) * kChunk;
-        const int64_t end = first + kChunk < e.n ? first + kChunk : e.n;
+        const int64_t first = (c - e.chunk0) * t.chunk;
+        const int64_t end = first + t.chunk < e.n ? first + t.chunk : e.n;
 #pragma unroll 2
         for (int64_t i = first + kVec * threadIdx.x; i < end; i += kVec * kThreads) {
             float v[8];
@@ -144,8 +147,8 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t c = t.chunks - 1 - k;
         const ClipEntry &e = t.e[tensor_of(t, c)];
         if (!scale && e.dst == e.src) continue;         // in place and nothing to change
-        const int64_t first = (c - e.chunk0) * kChunk;
-        const int64_t end = first + kChunk < e.n ? first + kChunk : e.n;
+        const int64_t first = (c - e.chunk0) * t.chunk;
+        const int64_t end = first + t.chunk < e.n ? first + t.chunk : e.n;
 #pragma unroll 2
         for (int64_t i = first + kVec * threadIdx.x; i < end; i += kVec * kThreads) {
             const int valid = static_cast<int>(end - i < 8 ? end - i : 8);
@@ -187,7 +190,7 @@ int32_t fill(const ufp4_tensor_t *tensors, int32_t first, int32_t n, ClipTable<M
         e.src_bf16 = s.src_dtype == UFP4_DTYPE_BF16;
         e.dst_bf16 = s.dst_dtype == UFP4_DTYPE_BF16;
         e.vec = ((reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst)) & 15u) == 0;
-        t->chunks += (s.n + kChunk - 1) / kChunk;
+        t->chunks += (s.n + t->chunk - 1) / t->chunk;
     }
     return i - first;
 }
@@ -196,6 +199,10 @@ template <int MAX>
 cudaError_t run(const ufp4_tensor_t *tensors, int32_t n, double *sums, bool scale, float max_norm, float *norm,
                 cudaStream_t stream) {
     ClipTable<MAX> t;
+    int64_t total = 0;
+    for (int32_t i = 0; i < n; ++i) total += tensors[i].n;
+    t.chunk = kChunkMax;
+    while (t.chunk > kChunkMin && total < t.chunk * kClipBlocks) t.chunk /= 2;
     int64_t count = 0;
     for (int32_t i = 0; i < n;) {
         i += fill(tensors, i, n, &t);

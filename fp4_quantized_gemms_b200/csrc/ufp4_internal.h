@@ -275,7 +275,7 @@ struct ClipEntry {
 };
 template <int MAX>
 struct ClipTable {
-    int64_t chunks;
+    int64_t chunks, chunk;       // how many, and their elements
     int32_t n;
     ClipEntry e[MAX];
 };
