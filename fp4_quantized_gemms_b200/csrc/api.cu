@@ -200,6 +200,36 @@ ufp4_status_t encode_operand_maps(const ufp4_qtensor_t *q, int code_rows, int sc
     return r == CUDA_SUCCESS ? UFP4_OK : UFP4_ERR_CUDA;
 }
 
+// The CTA-pair kernels move the epilogue's tensors by bulk tensor copies, a
+// warp's 32 x 32 piece at a time, through 4 KB of shared memory per warp: a
+// piece of the output, where the residual of the same type arrives first, and
+// one of the stored pre-activation.  So all are bf16, or the output (and the
+// residual) fp32 without a stored pre-activation; and bulk copies need
+// 16-byte aligned rows.  Everything else takes the kernels' element-wise path.
+ufp4_status_t encode_epilogue_maps(GemmArgs *args, int mode, int64_t m, int64_t n) {
+    EpiArgs &e = args->epi;
+    auto fits = [m](const void *p, int64_t ld, bool bf16) {
+        return aligned16(p) && (m == 1 || ld * (bf16 ? 2 : 4) % 16 == 0) && ld < (int64_t(1) << 36);
+    };
+    e.tma = mode >= 5 && fits(e.out, e.ld_out, e.out_bf16) &&
+            (e.residual == nullptr || (fits(e.residual, e.ld_res, e.res_bf16) && e.res_bf16 == e.out_bf16)) &&
+            (e.pre == nullptr || (fits(e.pre, e.ld_pre, e.pre_bf16) && e.pre_bf16 && e.out_bf16));
+    if (!e.tma) return UFP4_OK;
+    auto encode = [&](CUtensorMap *map, const void *p, int64_t ld, bool bf16) {
+        return encode_tensor_map_2d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p,
+                                    static_cast<uint64_t>(n), static_cast<uint64_t>(m),
+                                    static_cast<uint64_t>(ld) * (bf16 ? 2 : 4), 32, 32,
+                                    bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+    };
+    // (a single row may have any pitch; the map wants one that covers a row)
+    auto pitch = [&](int64_t ld, bool bf16) { return m > 1 ? ld : round_up(n, bf16 ? 8 : 4); };
+    if (!encode(&args->tm_out, e.out, pitch(e.ld_out, e.out_bf16), e.out_bf16) ||
+        (e.residual != nullptr && !encode(&args->tm_res, e.residual, pitch(e.ld_res, e.res_bf16), e.res_bf16)) ||
+        (e.pre != nullptr && !encode(&args->tm_pre, e.pre, pitch(e.ld_pre, true), true)))
+        return UFP4_ERR_CUDA;
+    return UFP4_OK;
+}
+
 ufp4_status_t run_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
                        const ufp4_group_t *groups_dev, int32_t num_groups, float *c, int64_t ldc,
                        int64_t m, int64_t n, void *stream, const EpiArgs *epi = nullptr) {
@@ -374,6 +404,8 @@ ufp4_status_t run_gemm(const ufp4_qtensor_t *a, const ufp4_qtensor_t *b,
     if (epi != nullptr) {
         args.epilogue = 1;
         args.epi = *epi;
+        s = encode_epilogue_maps(&args, mode, m, n);
+        if (s != UFP4_OK) return s;
     }
     cudaError_t e = launch_gemm(args, mode, grid_kind, sm_count(), st);
     return e == cudaSuccess ? UFP4_OK : UFP4_ERR_CUDA;
@@ -861,8 +893,6 @@ ufp4_status_t ufp4_gemm_epilogue(const ufp4_qtensor_t *a, const ufp4_qtensor_t *
             e.vec_pre = row_vec(epi->pre, epi->pre_dtype, epi->ld_pre, 4);
         }
     }
-    e.vec_all = e.vec_out && (e.bias == nullptr || e.vec_bias) && (e.residual == nullptr || e.vec_res) &&
-                (e.pre == nullptr || e.vec_pre);
     return run_gemm(a, b, nullptr, 0, nullptr, 0, m, n, stream, &e);
 }
 

@@ -1203,13 +1203,16 @@ struct PairCfg {
     static constexpr int o_scr = o_out + kOutBytes;
     static constexpr int o_bar = o_scr + kScr;
     // full[NS], empty[NS], sfull[NS], sfready[NS], sflocal[NS], acc_full,
-    // acc_empty, drain
-    static constexpr int kNumBars = 5 * NS + 3;
+    // acc_empty, drain, residual landed [8 epilogue warps][2 slots]
+    static constexpr int kNumBars = 5 * NS + 3 + 16;
     static constexpr int o_misc = o_bar + kNumBars * 8;
     static constexpr int kMaxOrder = 256;           // grouped problems: a schedule of up to 256 groups
     static constexpr int o_cum = o_misc + 64;       // int64 [kMaxOrder + 1]
     static constexpr int o_order = o_cum + 8 * (kMaxOrder + 1);   // u16 [kMaxOrder]
     static constexpr int kAlloc = o_order + 2 * kMaxOrder + 1024;
+    // Dense problems with an epilogue have no schedule: two tiles' bias there.
+    static constexpr int o_bias = (o_cum + 15) / 16 * 16;         // fp32 [2][256]
+    static_assert(o_bias + 2 * 256 * 4 <= o_order + 2 * kMaxOrder, "bias in the schedule's place");
     static constexpr int kThreads = 32 * 12;
     static_assert(NS >= 4, "pipeline depth");
     static_assert(kAlloc <= 232448, "shared memory budget");
@@ -1338,10 +1341,174 @@ __device__ __forceinline__ void store_piece(const GemmArgs &args, const Tile &tl
     }
 }
 
-// The same piece through the epilogue (EpiArgs): always transposed through the
-// buffer, so that a lane finishes four consecutive columns of a row, the same
-// four of eight rows: the bias is loaded once per piece, and residual, pre and
-// out move in whole 32-byte sectors.
+// ---- The epilogue (EpiArgs) of the pair kernels.
+//
+// Fast path (epi.tma): a thread keeps its accumulator row, so the bias is the
+// same for the whole warp (fp32 in shared memory, one broadcast read per four
+// columns) and the activation runs in place.  A piece of 32 rows x 32 columns
+// leaves through the warp's 4 KB buffer by one bulk tensor store, and the
+// residual arrives there by a bulk tensor load that was issued a piece (for
+// the first piece: a tile) earlier; each thread adds its row and overwrites it
+// with the result.  The copies clip rows and columns outside the matrix.  A
+// first form finished four columns of eight rows per lane with ordinary
+// accesses: 20 instructions per element against 11, and 298 against 170 us
+// for the MX product 8192 x 8192 x 2048 with GELU, bias and pre-activation.
+//
+// Buffer: two slots of 2 KB for bf16 pieces (out in turn, or slot 0 out and
+// slot 1 pre), one of 4 KB for fp32 pieces.  16-byte unit u of row r sits at
+// unit u ^ ((r / 2) % 4) (bf16) or u ^ (r % 8) (fp32): the copies' swizzles,
+// conflict-free when 32 rows are written at once.
+struct EpiWarp {
+    uint8_t *buf;          // 4 KB, 1024-byte aligned
+    uint64_t *bars;        // residual landed: one per slot
+    uint32_t phase;        // bit s: parity of slot s's next wait
+    uint32_t pending;      // bit s: a residual load into slot s is in flight
+};
+
+__device__ __forceinline__ bool epi_two_slots(const EpiArgs &e) { return e.out_bf16 && e.pre == nullptr; }
+
+// Starts the residual load of the piece at (col, row) into a slot that no
+// store reads any more.
+__device__ __forceinline__ void epi_load_residual(const GemmArgs &args, EpiWarp &w, int lane, int slot, int64_t col,
+                                                  int64_t row) {
+    if (lane == 0) {
+        mbar_arrive_expect_tx(&w.bars[slot], args.epi.out_bf16 ? 2048 : 4096);
+        tma_load_2d(w.buf + 2048 * slot, &args.tm_res, &w.bars[slot], static_cast<int32_t>(col),
+                    static_cast<int32_t>(row));
+    }
+    w.pending |= 1u << slot;
+}
+
+// Waits (with a limit) for loads in flight before the warp gives up its buffer.
+__device__ __forceinline__ void epi_drain(EpiWarp &w, int lane) {
+    if (lane == 0) {
+        uint32_t dummy = 0;
+        for (int s = 0; s < 2; ++s)
+            if (w.pending >> s & 1u) mbar_wait(&w.bars[s], w.phase >> s & 1u, kErrTimeoutDrain, &dummy);
+        bulk_wait_all();
+    }
+}
+
+// 32 columns of a thread's row, bf16, to a slot.
+__device__ __forceinline__ void epi_stage_bf16(uint8_t *slot, int lane, const float (&v)[32]) {
+    uint8_t *rowp = slot + lane * 64;
+    const int x = (lane >> 1) & 3;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4 *>(rowp + ((u ^ x) << 4)) =
+            make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
+                       pack_bf16(v[8 * u + 4], v[8 * u + 5]), pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+}
+
+// The pieces of a warp's 32 accumulator rows x 32 NP columns from col0.
+// Returns false when a wait gave up.
+template <int ACT, int NP>
+__device__ __forceinline__ bool epilogue_pieces(const GemmArgs &args, EpiWarp &w, int lane, const float *bias,
+                                                int64_t row0, int64_t col0, int64_t n, uint32_t (&r)[NP][32], float mult,
+                                                volatile uint32_t *abort_flag) {
+    const EpiArgs &e = args.epi;
+    const bool res = e.residual != nullptr, two = epi_two_slots(e);
+#pragma unroll
+    for (int c = 0; c < NP; ++c) {
+        const int64_t col = col0 + 32 * c;
+        if (col >= n) break;                          // the same for the whole warp
+        const int slot = two ? c & 1 : 0;
+        // the next piece's residual goes to the slot that the last piece's
+        // store has been read from
+        if (res && two && c + 1 < NP && col + 32 < n) {
+            if (lane == 0) bulk_wait_read<0>();
+            epi_load_residual(args, w, lane, (c + 1) & 1, col + 32, row0);
+        }
+        float v[32];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 b = *reinterpret_cast<const float4 *>(bias + 32 * c + 4 * q);
+            v[4 * q] = fmaf(__uint_as_float(r[c][4 * q]), mult, b.x);
+            v[4 * q + 1] = fmaf(__uint_as_float(r[c][4 * q + 1]), mult, b.y);
+            v[4 * q + 2] = fmaf(__uint_as_float(r[c][4 * q + 2]), mult, b.z);
+            v[4 * q + 3] = fmaf(__uint_as_float(r[c][4 * q + 3]), mult, b.w);
+        }
+        if (!res || e.pre != nullptr) {               // slots free again (a slot with a residual is)
+            if (lane == 0) {
+                if (two && c > 0)                     // the last piece's store has the other slot
+                    bulk_wait_read<1>();
+                else
+                    bulk_wait_read<0>();
+            }
+            __syncwarp();
+        }
+        if (e.pre != nullptr) epi_stage_bf16(w.buf + 2048, lane, v);
+        if constexpr (ACT != UFP4_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], ACT);
+        }
+        uint8_t *piece = w.buf + 2048 * slot;
+        if (res) {
+            if (!warp_wait(&w.bars[slot], w.phase >> slot & 1u, kErrTimeoutEpilogue, abort_flag)) return false;
+            w.phase ^= 1u << slot;
+            w.pending &= ~(1u << slot);
+        }
+        if (e.out_bf16) {
+            if (res) {
+                const uint8_t *rowp = piece + lane * 64;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(rowp + ((u ^ ((lane >> 1) & 3)) << 4));
+                    const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[8 * u + 2 * k] += bf16_lo(qw[k]);
+                        v[8 * u + 2 * k + 1] += bf16_hi(qw[k]);
+                    }
+                }
+            }
+            epi_stage_bf16(piece, lane, v);
+        } else {
+            uint8_t *rowp = piece + lane * 128;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                float4 *p = reinterpret_cast<float4 *>(rowp + ((u ^ (lane & 7)) << 4));
+                float4 o = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+                if (res) o = add_quad(o, *p);
+                *p = o;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(&args.tm_out, piece, static_cast<int32_t>(col), static_cast<int32_t>(row0));
+            if (e.pre != nullptr)
+                tma_store_2d(&args.tm_pre, w.buf + 2048, static_cast<int32_t>(col), static_cast<int32_t>(row0));
+            bulk_commit();
+        }
+        if (res && !two && c + 1 < NP && col + 32 < n) {
+            if (lane == 0) bulk_wait_read<0>();
+            epi_load_residual(args, w, lane, 0, col + 32, row0);
+        }
+    }
+    return true;
+}
+
+template <int NP>
+__device__ __forceinline__ bool epilogue_rows(const GemmArgs &args, EpiWarp &w, int lane, const float *bias,
+                                              int64_t row0, int64_t col0, int64_t n, uint32_t (&r)[NP][32], float mult,
+                                              volatile uint32_t *abort_flag) {
+    switch (args.epi.act) {
+        case UFP4_ACT_RELU:
+            return epilogue_pieces<UFP4_ACT_RELU>(args, w, lane, bias, row0, col0, n, r, mult, abort_flag);
+        case UFP4_ACT_GELU:
+            return epilogue_pieces<UFP4_ACT_GELU>(args, w, lane, bias, row0, col0, n, r, mult, abort_flag);
+        case UFP4_ACT_GELU_ERF:
+            return epilogue_pieces<UFP4_ACT_GELU_ERF>(args, w, lane, bias, row0, col0, n, r, mult, abort_flag);
+        case UFP4_ACT_SILU:
+            return epilogue_pieces<UFP4_ACT_SILU>(args, w, lane, bias, row0, col0, n, r, mult, abort_flag);
+        default:
+            return epilogue_pieces<UFP4_ACT_NONE>(args, w, lane, bias, row0, col0, n, r, mult, abort_flag);
+    }
+}
+
+// Any types, pitches and alignments: a piece is transposed through the buffer
+// as fp32, and a lane finishes four columns of a row at a time.
 __device__ __forceinline__ void stage_piece(uint8_t *buf, int lane, const uint32_t (&r)[32], float mult) {
     uint8_t *rowp = buf + lane * 128;
 #pragma unroll
@@ -1352,79 +1519,9 @@ __device__ __forceinline__ void stage_piece(uint8_t *buf, int lane, const uint32
                         __fmul_rn(__uint_as_float(r[4 * ch + 3]), mult));
 }
 
-// Residual of four rows (4 apart) as loaded.
-struct ResidualRows {
-    uint4 w[4];
-    __device__ __forceinline__ void load(const EpiArgs &e, int64_t row, int64_t col, int64_t m) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (row + 4 * k < m) {
-                const int64_t i = (row + 4 * k) * e.ld_res + col;
-                if (e.res_bf16) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(e.residual) + i);
-                    w[k].x = u.x;
-                    w[k].y = u.y;
-                } else {
-                    w[k] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(e.residual) + i);
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ float4 get(const EpiArgs &e, int k) const {
-        return e.res_bf16 ? make_float4(bf16_lo(w[k].x), bf16_hi(w[k].x), bf16_lo(w[k].y), bf16_hi(w[k].y))
-                          : make_float4(__uint_as_float(w[k].x), __uint_as_float(w[k].y), __uint_as_float(w[k].z),
-                                        __uint_as_float(w[k].w));
-    }
-};
-
-// A staged piece whose 32 columns all exist and whose rows take vector
-// accesses.  The activation is chosen outside the row loop and the loop is
-// kept short (four rows per turn): every epilogue warp runs through this code
-// for each piece, and an earlier form with the choice inside and everything
-// unrolled spent its time fetching instructions (one 256 x 512 x 512 MX product
-// with GELU, bias and residual: 41 us, now 26).  The residual of the next four
-// rows is on its way while four rows are finished.
-template <int ACT>
-__device__ __forceinline__ void finish_piece(const EpiArgs &e, const uint8_t *buf, int lane, int64_t m0, int64_t m,
-                                             int64_t gcol) {
-    const int c16 = lane & 7, r0 = lane >> 3;
-    const float4 bias = e.bias != nullptr ? load_quad(e.bias, gcol, e.bias_bf16, true, 4)
-                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const bool has_res = e.residual != nullptr;
-    ResidualRows res;
-    if (has_res) res.load(e, m0 + r0, gcol, m);
-#pragma unroll 1
-    for (int k0 = 0; k0 < 32; k0 += 16) {
-        const ResidualRows cur = res;
-        if (has_res && k0 == 0) res.load(e, m0 + 16 + r0, gcol, m);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int rr = k0 + 4 * k + r0;
-            const float4 v = *reinterpret_cast<const float4 *>(buf + rr * 128 + ((c16 ^ (rr & 7)) << 4));
-            float4 z = add_quad(v, bias);
-            const bool ok = m0 + rr < m;
-            if (e.pre != nullptr && ok) store_quad(e.pre, (m0 + rr) * e.ld_pre + gcol, e.pre_bf16, true, 4, z);
-            if constexpr (ACT != UFP4_ACT_NONE)
-                z = make_float4(act_value(z.x, ACT), act_value(z.y, ACT), act_value(z.z, ACT), act_value(z.w, ACT));
-            if (has_res) z = add_quad(z, cur.get(e, k));
-            if (ok) store_quad(e.out, (m0 + rr) * e.ld_out + gcol, e.out_bf16, true, 4, z);
-        }
-    }
-}
-
-__device__ __forceinline__ void epilogue_piece(const EpiArgs &e, const uint8_t *buf, int lane, int64_t m0,
-                                               int64_t col0, int64_t m, int64_t n) {
+__device__ __forceinline__ void epilogue_piece_any(const EpiArgs &e, const uint8_t *buf, int lane, int64_t m0,
+                                                   int64_t col0, int64_t m, int64_t n) {
     const int64_t gcol = col0 + 4 * (lane & 7);
-    if (e.vec_all && col0 + 32 <= n) {                // the same for the whole warp
-        switch (e.act) {
-            case UFP4_ACT_RELU: finish_piece<UFP4_ACT_RELU>(e, buf, lane, m0, m, gcol); break;
-            case UFP4_ACT_GELU: finish_piece<UFP4_ACT_GELU>(e, buf, lane, m0, m, gcol); break;
-            case UFP4_ACT_GELU_ERF: finish_piece<UFP4_ACT_GELU_ERF>(e, buf, lane, m0, m, gcol); break;
-            case UFP4_ACT_SILU: finish_piece<UFP4_ACT_SILU>(e, buf, lane, m0, m, gcol); break;
-            default: finish_piece<UFP4_ACT_NONE>(e, buf, lane, m0, m, gcol); break;
-        }
-        return;
-    }
     const int valid = gcol + 4 <= n ? 4 : static_cast<int>(n - gcol);   // <= 0: outside
     const float4 bias = epilogue_bias(e, gcol, valid);
 #pragma unroll 1
@@ -1451,6 +1548,7 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
     uint64_t *acc_full = sflocal + NS;    // accumulator complete (commit to both CTAs)
     uint64_t *acc_empty = acc_full + 1;   // leader: both CTAs' epilogues drained TMEM (8 or 16 warps)
     uint64_t *drain = acc_empty + 1;
+    uint64_t *epi_bars = drain + 1;       // [epilogue warp][slot]: residual piece landed
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::o_misc);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + C::o_misc + 4);
     auto stage = [&](int s) { return smem + s * C::kStage; };
@@ -1474,6 +1572,8 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, ATOMS ? 16 : 8);
         mbar_init(drain, 1);
+        if constexpr (EPI)
+            for (int i = 0; i < 16; ++i) mbar_init(&epi_bars[i], 1);
         *abort_flag = 0u;
         fence_barrier_init();
     }
@@ -1780,17 +1880,47 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
         const float mult = C::kMx ? args.inv_n
                                   : __fmul_rn(__fmul_rn(*args.a_S, *args.b_S),
                                               args.inv_n * (GRID == 0 ? (1.0f / 16.0f) : 1.0f));
+        const int ewarp = warp - (ATOMS ? 4 : 8);
+        EpiWarp ew{buf, epi_bars + 2 * ewarp, 0u, 0u};
         uint32_t tcount = 0;
         for (int64_t t = unit; t < ntiles; t += nunits, ++tcount) {
             const Tile tl = get_tile<TM, BN>(args, t, sched);
+            const int64_t m0 = tl.m0 + 128 * rank + 32 * q;   // this warp's accumulator rows
+            bool ok = true;
+            // The tile's bias as fp32: every epilogue warp writes the columns
+            // that it reads (the same values as its neighbours), in two
+            // buffers in turn: a warp is at most one tile ahead of another
+            // that still reads (the accumulator is full only after all have
+            // emptied it).  The first residual piece starts its way now.
+            float *bias_s = reinterpret_cast<float *>(smem + C::o_bias) + 256 * (tcount & 1);
+            if constexpr (EPI) {
+                if (args.epi.tma) {
+#pragma unroll
+                    for (int hh = 0; hh < kHalves; ++hh) {
+                        const int col = 128 * (h0 + hh) + 4 * lane;
+                        const int64_t left = tl.g.n - (tl.n0 + col);
+                        const int valid = left < 0 ? 0 : left < 4 ? static_cast<int>(left) : 4;
+                        *reinterpret_cast<float4 *>(bias_s + col) = epilogue_bias(args.epi, tl.n0 + col, valid);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (EPI && args.epi.tma && args.epi.residual != nullptr && m0 < tl.g.m && tl.n0 + 128 * h0 < tl.g.n) {
+                if (lane == 0) bulk_wait_read<0>();
+                epi_load_residual(args, ew, lane, 0, tl.n0 + 128 * h0, m0);
+            }
             if (!warp_wait(acc_full, tcount & 1, kErrTimeoutEpilogue, abort_flag)) break;
             tc_fence_after();
-            const int64_t m0 = tl.m0 + 128 * rank + 32 * q;   // this warp's accumulator rows
             const bool vec_tile = args.c_vec && (tl.g.c_col & 3) == 0;
             const bool zero = tl.g.k == 0;             // no MMA wrote the accumulator
 #pragma unroll
             for (int hh = 0; hh < kHalves; ++hh) {
                 const int h = h0 + hh;
+                if (EPI && hh > 0 && args.epi.tma && args.epi.residual != nullptr && m0 < tl.g.m &&
+                    tl.n0 + 128 * h < tl.g.n) {
+                    if (lane == 0) bulk_wait_read<0>();
+                    epi_load_residual(args, ew, lane, 0, tl.n0 + 128 * h, m0);
+                }
                 uint32_t r[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tmem_base + lane_addr + 128 * h + 32 * c, r[c]);
@@ -1805,6 +1935,12 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
                                      : "memory");
                 }
                 if constexpr (EPI) {
+                    if (args.epi.tma) {
+                        if (m0 < tl.g.m && ok)
+                            ok = epilogue_rows<4>(args, ew, lane, bias_s + 128 * h, m0, tl.n0 + 128 * h, tl.g.n, r, mult,
+                                                  abort_flag);
+                        continue;
+                    }
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         const int64_t col0 = tl.n0 + 128 * h + 32 * c;
@@ -1816,7 +1952,7 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
                             default: stage_piece(buf, lane, r[3], mult); break;
                         }
                         __syncwarp();
-                        epilogue_piece(args.epi, buf, lane, m0, col0, tl.g.m, tl.g.n);
+                        epilogue_piece_any(args.epi, buf, lane, m0, col0, tl.g.m, tl.g.n);
                         __syncwarp();                     // buffer read out before the next piece
                     }
                 } else {
@@ -1828,7 +1964,9 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
                     }
                 }
             }
+            if (!ok) break;
         }
+        if constexpr (EPI) epi_drain(ew, lane);
     }
 
     tc_fence_before();

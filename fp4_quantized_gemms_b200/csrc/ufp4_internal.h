@@ -125,7 +125,7 @@ struct EpiArgs {
     int64_t ld_res, ld_pre, ld_out;
     int32_t bias_bf16, res_bf16, pre_bf16, out_bf16;   // else fp32
     int32_t vec_bias, vec_res, vec_pre, vec_out;
-    int32_t vec_all;         // all of those that are present
+    int32_t tma;             // CTA-pair kernels: the tensors move by bulk tensor copies (maps below)
     int32_t act;             // ufp4_act_t
 };
 
@@ -154,6 +154,7 @@ struct GemmArgs {
     int lanes;                            // A carries per-lane factor tiles (E1M2 pair kernel)
     int atoms;                            // both operands carry factor atoms (pair kernels, dense)
     int band;                             // tile order: rows of tiles per band (0: M fastest)
+    CUtensorMap tm_out, tm_res, tm_pre;   // epilogue tensors, boxes of 32 rows x 32 columns (epi.tma)
     int epilogue;                         // dense problems: `epi` replaces the plain fp32 store to c
     EpiArgs epi;
 };
