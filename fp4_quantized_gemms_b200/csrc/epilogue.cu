@@ -28,17 +28,21 @@ namespace {
 constexpr int kBwdThreads = 256;
 constexpr int kBwdWarps = kBwdThreads / 32;
 constexpr int kBwdCols = 256;      // columns of a block
-constexpr int kBwdUnroll = 4;      // rows of a warp in flight
+// Rows of a warp in flight: 128 to 192 bytes per lane, within the registers of
+// three blocks per SM.
+template <bool DOUT_BF16, bool PRE_BF16>
+constexpr int kBwdUnroll = DOUT_BF16 && PRE_BF16 ? 4 : DOUT_BF16 || PRE_BF16 ? 3 : 2;
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void *p, int64_t i, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void *p, int64_t i, const float2 (&v)[4]) {
     if constexpr (BF16) {
         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
+                       pack_bf16(v[3].x, v[3].y));
     } else {
         float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     }
 }
 
@@ -61,23 +65,24 @@ __device__ __forceinline__ void store_partial(const EpiBwdArgs &a, const float (
 }
 
 template <int ACT, bool DOUT_BF16, bool PRE_BF16, bool DPRE_BF16>
-__global__ void __launch_bounds__(kBwdThreads) epilogue_backward_kernel(const __grid_constant__ EpiBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, 3) epilogue_backward_kernel(const __grid_constant__ EpiBwdArgs a) {
     let_next_kernel_launch();
+    constexpr int U = kBwdUnroll<DOUT_BF16, PRE_BF16>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kBwdCols;
     const int64_t col = col0 + 8 * lane;
     const bool col_ok = col < a.n;                     // n % 8 == 0: all eight or none
     const int64_t r_first = blockIdx.y * a.rows_per_chunk + warp;
     const int64_t r_end = min(a.m, (blockIdx.y + 1) * a.rows_per_chunk);
-    float sum[8];
+    float2 sum[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    for (int j = 0; j < 4; ++j) sum[j] = splat(0.0f);
     if (col_ok) {
-        for (int64_t r0 = r_first; r0 < r_end; r0 += kBwdWarps * kBwdUnroll) {
-            Raw8<DOUT_BF16> g[kBwdUnroll];
-            Raw8<PRE_BF16> z[kBwdUnroll];
+        for (int64_t r0 = r_first; r0 < r_end; r0 += kBwdWarps * U) {
+            Raw8<DOUT_BF16> g[U];
+            Raw8<PRE_BF16> z[U];
 #pragma unroll
-            for (int u = 0; u < kBwdUnroll; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int64_t r = r0 + kBwdWarps * u;
                 if (r < r_end) {
                     g[u].load(a.dout, r * a.ld_dout + col);
@@ -85,24 +90,25 @@ __global__ void __launch_bounds__(kBwdThreads) epilogue_backward_kernel(const __
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kBwdUnroll; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int64_t r = r0 + kBwdWarps * u;
                 if (r < r_end) {
-                    float d[8], zv[8];
-                    g[u].get(d);
+                    float2 d[4], zv[4];
+                    g[u].get2(d);
                     if constexpr (ACT != UFP4_ACT_NONE) {
-                        z[u].get(zv);
+                        z[u].get2(zv);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) d[j] *= act_slope<ACT>(zv[j]);
+                        for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], act_slope2<ACT>(zv[j]));
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += d[j];
+                    for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], d[j]);
                     if (a.dpre != nullptr) store8<DPRE_BF16>(a.dpre, r * a.ld_dpre + col, d);
                 }
             }
         }
     }
-    if (a.dbias != nullptr) store_partial<true>(a, sum, col0);
+    const float sums[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
+    if (a.dbias != nullptr) store_partial<true>(a, sums, col0);
 }
 
 // Any width, row pitch and alignment: one element per access, a warp's 32
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(kBwdThreads) epilogue_backward_any_kernel(cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t col = col0 + lane + 32 * j;
-            if constexpr (ACT != UFP4_ACT_NONE) d[j] *= act_slope<ACT>(z[j]);
+            if constexpr (ACT != UFP4_ACT_NONE) d[j] *= act_slope2<ACT>(splat(z[j])).x;
             sum[j] += d[j];
             if (a.dpre != nullptr && col < a.n) store_elem(a.dpre, r * a.ld_dpre + col, a.dpre_bf16, d[j]);
         }

@@ -141,17 +141,34 @@ struct RowShape {
     static constexpr int kThreads = kRowThreads * kRows;
 };
 
+// max(|a|, |b|, |c|)
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
+// Where a row's scale bytes and atom bytes go; block b of the row is at
+// scales[b * scale_ld] and atoms[b / 4 * 512 + b % 4].
+struct RowFactors {
+    uint8_t *scales, *atoms;
+    __device__ __forceinline__ RowFactors(const NormArgs &a, int64_t row) {
+        scales = a.scales + row;
+        atoms = a.sf_atoms == nullptr ? nullptr
+                                      : a.sf_atoms + (row / 128) * a.atoms_k * 512 + 16 * (row % 32) + 4 * ((row / 32) % 4);
+    }
+};
+
 // Writes eight columns of a row's output, y = h r w: bf16, or E4M3 elements and
 // their blocks' factors (all lanes of the warp take part: a block of 32
 // elements is four neighbouring lanes; elements beyond the row are 0).
 template <bool OUT8, bool VEC>
-__device__ __forceinline__ void write_y(const NormArgs &a, int64_t row, int64_t col, int valid, const float (&v)[8]) {
+__device__ __forceinline__ void write_y(const NormArgs &a, const RowFactors &f, int64_t row, int col, int valid,
+                                        const float (&v)[8]) {
     if constexpr (!OUT8) {
         put8<true, VEC>(a.y, row * a.ld_y + col, valid, v);
     } else {
-        float amax = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        float amax = max_abs3(max_abs3(max_abs3(v[0], v[1], v[2]), v[3], v[4]), max_abs3(v[5], v[6], v[7]), 0.0f);
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
         const int x = block_exponent(amax);
@@ -160,17 +177,14 @@ __device__ __forceinline__ void write_y(const NormArgs &a, int64_t row, int64_t 
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                p[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e] * inv, v[2 * e + 1] * inv), __NV_SATFINITE,
+                p[e] = __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[2 * e], v[2 * e + 1]), splat(inv)), __NV_SATFINITE,
                                                 __NV_E4M3);
             *reinterpret_cast<uint2 *>(a.elems8 + row * a.kpad + col) =
                 make_uint2(plain_zeros(p[0] | (p[1] << 16)), plain_zeros(p[2] | (p[3] << 16)));
             if ((threadIdx.x & 3) == 0) {
-                const int64_t b = col / 32;
-                const uint8_t byte = static_cast<uint8_t>(x + 127);
-                a.scales[b * a.scale_ld + row] = byte;
-                if (a.sf_atoms != nullptr)
-                    a.sf_atoms[((row / 128) * a.atoms_k + b / 4) * 512 + 16 * (row % 32) + 4 * ((row / 32) % 4) +
-                               b % 4] = byte;
+                const int b = col >> 5;
+                f.scales[b * a.scale_ld] = static_cast<uint8_t>(x + 127);
+                if (f.atoms != nullptr) f.atoms[(b >> 2) * 512 + (b & 3)] = static_cast<uint8_t>(x + 127);
             }
         }
     }
@@ -210,6 +224,14 @@ __device__ __forceinline__ void load8s(const uint8_t *p, int col, bool ok, float
     load8<BF16, true>(p, col, ok ? 8 : 0, v);
 }
 
+template <bool BF16>
+__device__ __forceinline__ void load8s(const uint8_t *p, int col, bool ok, float2 (&v)[4]) {
+    float f[8];
+    load8<BF16, true>(p, col, ok ? 8 : 0, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
+}
+
 template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8>
 __global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -238,11 +260,14 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_const
     __syncthreads();
     if (t == 0)
         for (int64_t k = 0; k < a.stages && k < n; ++k) issue(k);
-    float w[NV][8];
+    float2 w[NV][4];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int col = 8 * (t + 32 * W * j);
-        load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, w[j]);
+        float v[8];
+        load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[j][e] = make_float2(v[2 * e], v[2 * e + 1]);
     }
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     int s = 0;
@@ -253,36 +278,53 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_const
         const int64_t row = blockIdx.x + k * gridDim.x;
         bad = !mbar_wait(&st.full[s], parity, kErrTimeoutTransform, &st.abort);
         const uint8_t *buf = ring + s * a.stage_bytes;
-        float h[NV][8];
-        float sum = 0.0f;
+        float2 h[NV][4], sq = splat(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = 8 * (t + 32 * W * j);
             load8s<XBF16>(buf, col, col < cols, h[j]);
             if constexpr (RES) {
-                float r[8];
+                float2 r[4];
                 load8s<SBF16>(buf + x_bytes, col, col < cols, r);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    h[j][e] += r[e];
-                    if constexpr (SBF16) h[j][e] = __bfloat162float(__float2bfloat16_rn(h[j][e]));
+                for (int e = 0; e < 4; ++e) h[j][e] = add2(h[j][e], r[e]);
+                if constexpr (SBF16) {                    // the stream as it is stored
+                    uint32_t hw[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        hw[e] = pack_bf16(h[j][e].x, h[j][e].y);
+                        h[j][e] = make_float2(bf16_lo(hw[e]), bf16_hi(hw[e]));
+                    }
+                    if (col < cols)
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.h) + row * a.ld_h + col) =
+                            make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                } else if (col < cols) {
+                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.h) + row * a.ld_h + col);
+                    dst[0] = make_float4(h[j][0].x, h[j][0].y, h[j][1].x, h[j][1].y);
+                    dst[1] = make_float4(h[j][2].x, h[j][2].y, h[j][3].x, h[j][3].y);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(h[j][e], h[j][e], sum);
+            for (int e = 0; e < 4; ++e) sq = fma2(h[j][e], h[j][e], sq);
         }
+        float sum = sq.x + sq.y;
         sum = row_sum<W>(sum, s_sum[k & 1], &bad);
         if (bad) break;
         if (t == 0 && k + a.stages < n) issue(k + a.stages);
         const float rstd = 1.0f / sqrtf(sum * inv_cols + a.eps);
         if (t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+        const RowFactors factors(a, row);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = 8 * (t + 32 * W * j);
-            if constexpr (RES) put8<SBF16, true>(a.h, row * a.ld_h + col, cols - col, h[j]);
+            float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * rstd * w[j][e];
-            write_y<OUT8, true>(a, row, col, cols - col, h[j]);
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = mul2(mul2(h[j][e], splat(rstd)), w[j][e]);
+                y[2 * e] = v.x;
+                y[2 * e + 1] = v.y;
+            }
+            write_y<OUT8, true>(a, factors, row, col, cols - col, y);
         }
         if (++s == a.stages) {
             s = 0;
@@ -322,15 +364,16 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_kernel(const __
     sum = row_sum<W>(sum, s_sum);
     const float rstd = 1.0f / sqrtf(sum * (1.0f / static_cast<float>(a.cols)) + a.eps);
     if (t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+    const RowFactors factors(a, row);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t col = 8 * (t + S::kRowThreads * j);
+        const int col = 8 * (t + S::kRowThreads * j);
         const int valid = col + 8 <= a.cols ? 8 : static_cast<int>(a.cols - col);
         float w[8];
         load_weight8(a.weight, a.weight_bf16, col, valid, a.vec_weight, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * rstd * w[e];
-        write_y<OUT8, VEC>(a, row, col, valid, h[j]);
+        write_y<OUT8, VEC>(a, factors, row, col, valid, h[j]);
     }
 }
 

@@ -53,14 +53,15 @@ __device__ __forceinline__ float group_sum(float v) {
 // Tokens that a group of lanes works on at a time: their loads and their
 // shuffle chains overlap.
 template <int J>
-constexpr int kTokensAtOnce = J <= 8 ? 4 : 1;
+constexpr int kTokensAtOnce = J <= 4 ? 4 : J <= 16 ? 2 : 1;
 
-// Softmax of U tokens' logits in registers; experts beyond E and tokens that
-// do not count (`live` false) give 0.  -inf logits give 0; a row of nothing
-// but -inf gives 0 everywhere.  NaN stays NaN.
+// exp(x - max) of U tokens' logits in registers, and each token's reciprocal
+// sum; experts beyond E and tokens that do not count (`live` false) give 0.
+// -inf logits give 0; a row of nothing but -inf gives 0 everywhere.  NaN
+// stays NaN.
 template <int G, int J, int V, bool BF16, int U>
-__device__ __forceinline__ void token_softmax(const BalanceArgs &a, const int64_t (&token)[U], const bool (&live)[U], int g,
-                                              float (&p)[U][J]) {
+__device__ __forceinline__ void token_exp(const BalanceArgs &a, const int64_t (&token)[U], const bool (&live)[U], int g,
+                                          float (&p)[U][J], float (&inv)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t base = token[u] * a.ld;
@@ -88,26 +89,35 @@ __device__ __forceinline__ void token_softmax(const BalanceArgs &a, const int64_
     for (int u = 0; u < U; ++u) m[u] = group_max<G>(m[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        // the difference first (exact near the maximum), then its base-2 exponent
         const float shift = m[u] == -CUDART_INF_F ? 0.0f : m[u];
-        s[u] = 0.0f;
+        if constexpr (J % 2 == 0) {
+            float2 sum = splat(0.0f);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            p[u][j] = __expf(p[u][j] - shift);
-            s[u] += p[u][j];
+            for (int j = 0; j < J; j += 2) {
+                const float2 x = mul2(add2(make_float2(p[u][j], p[u][j + 1]), splat(-shift)), splat(kLog2e));
+                p[u][j] = ex2_approx(x.x);
+                p[u][j + 1] = ex2_approx(x.y);
+                sum = add2(sum, make_float2(p[u][j], p[u][j + 1]));
+            }
+            s[u] = sum.x + sum.y;
+        } else {
+            s[u] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                p[u][j] = ex2_approx((p[u][j] - shift) * kLog2e);
+                s[u] += p[u][j];
+            }
         }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) s[u] = group_sum<G>(s[u]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const float inv = s[u] == 0.0f ? 0.0f : __fdividef(1.0f, s[u]);
-#pragma unroll
-        for (int j = 0; j < J; ++j) p[u][j] *= inv;
-    }
+    for (int u = 0; u < U; ++u) inv[u] = s[u] == 0.0f ? 0.0f : __fdividef(1.0f, s[u]);
 }
 
 template <int G, int J, int V, bool BF16>
-__global__ void __launch_bounds__(kThreads) balance_partial_kernel(const __grid_constant__ BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, J <= 16 ? 2 : 1) balance_partial_kernel(const __grid_constant__ BalanceArgs a) {
     extern __shared__ uint32_t s_mem[];
     const int E = a.experts;
     int32_t *s_count = reinterpret_cast<int32_t *>(s_mem);          // [E]
@@ -137,12 +147,12 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const __grid_
             live[u] = t[u] < a.tokens && (a.mask == nullptr || a.mask[t[u]] != 0);
             first[u] = live[u] && g < a.topk ? a.choices[t[u] * a.topk + g] : -1;
         }
-        float p[U][J];
-        token_softmax<G, J, V, BF16, U>(a, t, live, g, p);
+        float p[U][J], inv[U];
+        token_exp<G, J, V, BF16, U>(a, t, live, g, p, inv);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int j = 0; j < J; ++j) acc[j] += p[u][j];
+            for (int j = 0; j < J; ++j) acc[j] = fmaf(p[u][j], inv[u], acc[j]);
             mine += live[u] && g == 0;
             if (first[u] >= 0 && first[u] < E) atomicAdd(&s_count[first[u]], 1);
             if (live[u])
@@ -250,7 +260,7 @@ __global__ void __cluster_dims__(kFinishBlocks) __launch_bounds__(1024)
 }
 
 template <int G, int J, int V, bool BF16>
-__global__ void __launch_bounds__(kThreads) balance_backward_kernel(const __grid_constant__ BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, J <= 16 ? 2 : 1) balance_backward_kernel(const __grid_constant__ BalanceArgs a) {
     constexpr int kGroups = kThreads / G;
     const int g = threadIdx.x % G;
     const int E = a.experts;
@@ -273,8 +283,8 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const __grid
             t[u] = t0 + u * step + threadIdx.x / G;
             live[u] = t[u] < a.tokens && (a.mask == nullptr || a.mask[t[u]] != 0);
         }
-        float p[U][J], dot[U];
-        token_softmax<G, J, V, BF16, U>(a, t, live, g, p);
+        float p[U][J], inv[U], dot[U];
+        token_exp<G, J, V, BF16, U>(a, t, live, g, p, inv);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             dot[u] = 0.0f;
@@ -282,9 +292,11 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const __grid
             for (int j = 0; j < J; ++j) dot[u] = fmaf(p[u][j], ge[j], dot[u]);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) dot[u] = group_sum<G>(dot[u]);
+        for (int u = 0; u < U; ++u) dot[u] = group_sum<G>(dot[u]) * inv[u];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) p[u][j] *= inv[u];
 #pragma unroll
             for (int j = 0; j < J; j += V) {
                 const int e = expert_of<G, V>(g, j);
@@ -327,19 +339,19 @@ cudaError_t launch_shape(const BalanceArgs &a, bool backward, cudaStream_t strea
     return launch_early(balance_finish_kernel, dim3(kFinishBlocks), dim3(1024), stream, a, blocks, share, width);
 }
 
-// Experts to lanes.  Rows that allow vectors of four: the fewest lanes that
-// leave each at most four (E <= 128), then a warp with more; else one expert
-// at a time.
+// Experts to lanes.  Rows that allow vectors of four: 16 experts per lane where
+// there are enough of them (a token's sums then take the fewest shuffles per
+// expert), else a few lanes per token; other rows one expert at a time.
 template <bool BF16>
 cudaError_t launch_type(const BalanceArgs &a, bool backward, cudaStream_t stream) {
     const int E = a.experts;
     if (a.vec) {
         if (E <= 8) return launch_shape<2, 4, 4, BF16>(a, backward, stream);
-        if (E <= 16) return launch_shape<4, 4, 4, BF16>(a, backward, stream);
-        if (E <= 32) return launch_shape<8, 4, 4, BF16>(a, backward, stream);
-        if (E <= 64) return launch_shape<16, 4, 4, BF16>(a, backward, stream);
-        if (E <= 128) return launch_shape<32, 4, 4, BF16>(a, backward, stream);
-        if (E <= 256) return launch_shape<32, 8, 4, BF16>(a, backward, stream);
+        if (E <= 32) return launch_shape<4, 8, 4, BF16>(a, backward, stream);
+        if (E <= 64) return launch_shape<4, 16, 4, BF16>(a, backward, stream);
+        if (E <= 128) return launch_shape<8, 16, 4, BF16>(a, backward, stream);
+        if (E <= 256) return launch_shape<16, 16, 4, BF16>(a, backward, stream);
+        if (E <= 512) return launch_shape<32, 16, 4, BF16>(a, backward, stream);
         return launch_shape<32, 32, 4, BF16>(a, backward, stream);
     }
     if (E <= 8) return launch_shape<8, 1, 1, BF16>(a, backward, stream);

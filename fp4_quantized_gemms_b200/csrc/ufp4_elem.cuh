@@ -98,6 +98,12 @@ struct Raw8 {
         w[0] = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (!BF16) w[1] = w[0];
     }
+    __device__ __forceinline__ void get2(float2 (&v)[4]) const {
+        float f[8];
+        get(f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = make_float2(f[2 * j], f[2 * j + 1]);
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         if constexpr (BF16) {
             const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
@@ -164,32 +170,46 @@ __device__ __forceinline__ float4 act_quad(float4 z, int act) {
     return make_float4(act_value(z.x, act), act_value(z.y, act), act_value(z.z, act), act_value(z.w, act));
 }
 
-// Derivative of the activation.  With t = exp(-2u) (GELU) or exp(-z) (SiLU)
+// Two lanes of one packed fp32x2 operation each (the same IEEE results).
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// Derivative of the activation, two at a time.  With t = exp(-2u) (GELU) or exp(-z) (SiLU)
 // and s = 1 / (1 + t): d = s + z u2' s (t s), where t s = 1 - s without
 // cancellation and u2' = d(2u)/dz.  Beyond |z| = 9 (GELU) or 60 (SiLU) the
 // derivative is 0 or 1 to fp32; the clamp keeps t finite and every product in
 // range.
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
+__device__ __forceinline__ float2 act_slope2(float2 z) {
     if constexpr (ACT == UFP4_ACT_RELU) {
-        return z > 0.0f ? 1.0f : 0.0f;
-    } else if constexpr (ACT == UFP4_ACT_GELU) {
-        const float c = clamp_nan(z, 9.0f);
-        const float c2 = c * c;
-        const float t = ex2_approx(c * fmaf(-kGelu2B * kLog2e, c2, -kGelu2A * kLog2e));
-        const float s = rcp_approx(1.0f + t);
-        return fmaf(c * fmaf(3.0f * kGelu2B, c2, kGelu2A), t * (s * s), s);
+        return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+    } else if constexpr (ACT == UFP4_ACT_GELU || ACT == UFP4_ACT_SILU) {
+        constexpr bool kGelu = ACT == UFP4_ACT_GELU;
+        const float lim = kGelu ? 9.0f : 60.0f;
+        const float2 c = make_float2(clamp_nan(z.x, lim), clamp_nan(z.y, lim));
+        float2 arg, du = c;                              // log2 t; z d(2u)/dz
+        if constexpr (kGelu) {
+            const float2 c2 = mul2(c, c);
+            arg = mul2(c, fma2(splat(-kGelu2B * kLog2e), c2, splat(-kGelu2A * kLog2e)));
+            du = mul2(c, fma2(splat(3.0f * kGelu2B), c2, splat(kGelu2A)));
+        } else {
+            arg = mul2(splat(-kLog2e), c);
+        }
+        const float2 t = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+        const float2 d = add2(splat(1.0f), t);
+        const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        return fma2(du, mul2(t, mul2(s, s)), s);
     } else if constexpr (ACT == UFP4_ACT_GELU_ERF) {
-        const float c = clamp_nan(z, 9.0f);
-        return fmaf(c * 0.39894228040143268f, ex2_approx(-0.5f * kLog2e * c * c),
-                    0.5f * (1.0f + erff(0.70710678118654752f * c)));
-    } else if constexpr (ACT == UFP4_ACT_SILU) {
-        const float c = clamp_nan(z, 60.0f);
-        const float t = ex2_approx(-kLog2e * c);
-        const float s = rcp_approx(1.0f + t);
-        return fmaf(c, t * (s * s), s);
+        auto one = [](float v) {
+            const float c = clamp_nan(v, 9.0f);
+            return fmaf(c * 0.39894228040143268f, ex2_approx(-0.5f * kLog2e * c * c),
+                        0.5f * (1.0f + erff(0.70710678118654752f * c)));
+        };
+        return make_float2(one(z.x), one(z.y));
     } else {
-        return 1.0f;
+        return splat(1.0f);
     }
 }
 
