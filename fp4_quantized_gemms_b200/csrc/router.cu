@@ -116,6 +116,13 @@ __device__ __forceinline__ void token_exp(const BalanceArgs &a, const int64_t (&
     for (int u = 0; u < U; ++u) inv[u] = s[u] == 0.0f ? 0.0f : __fdividef(1.0f, s[u]);
 }
 
+// The token count and the loss from sum_e c_e (sum of p_e) and the count.
+__device__ __forceinline__ void write_loss(const BalanceArgs &a, double dot, int64_t tokens) {
+    const double n = static_cast<double>(tokens);
+    *a.valid_tokens = tokens;
+    *a.loss = tokens == 0 ? 0.0f : static_cast<float>(static_cast<double>(a.coef) * a.experts * dot / (n * n * a.topk));
+}
+
 template <int G, int J, int V, bool BF16>
 __global__ void __launch_bounds__(kThreads, J <= 16 ? 2 : 1) balance_partial_kernel(const __grid_constant__ BalanceArgs a) {
     extern __shared__ uint32_t s_mem[];
@@ -172,13 +179,33 @@ __global__ void __launch_bounds__(kThreads, J <= 16 ? 2 : 1) balance_partial_ker
     }
     if (mine != 0) atomicAdd(&s_tokens, mine);
     __syncthreads();
+    const bool alone = gridDim.x == 1;          // few tokens: the results themselves
+    double dot = 0.0;
     for (int e = threadIdx.x; e < E; e += kThreads) {
         float s = 0.0f;
         for (int w = 0; w < kWarps; ++w) s += s_prob[w * E + e];
-        a.part_prob[static_cast<int64_t>(blockIdx.x) * E + e] = s;
-        a.part_count[static_cast<int64_t>(blockIdx.x) * E + e] = s_count[e];
+        if (alone) {
+            a.counts[e] = s_count[e];
+            dot += static_cast<double>(s_count[e]) * static_cast<double>(s);
+        } else {
+            a.part_prob[static_cast<int64_t>(blockIdx.x) * E + e] = s;
+            a.part_count[static_cast<int64_t>(blockIdx.x) * E + e] = s_count[e];
+        }
     }
-    if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = s_tokens;
+    if (!alone) {
+        if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = s_tokens;
+        return;
+    }
+    __shared__ double s_dot[kWarps];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+    if (lane == 0) s_dot[warp] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double d = 0.0;
+        for (int w = 0; w < kWarps; ++w) d += s_dot[w];
+        write_loss(a, d, s_tokens);
+    }
 }
 
 // Adds the partial rows; writes counts, the token count and the loss.  One
@@ -251,10 +278,7 @@ __global__ void __cluster_dims__(kFinishBlocks) __launch_bounds__(1024)
         int64_t n = 0;
         for (int r = 0; r < kFinishBlocks; ++r) d += *cluster.map_shared_rank(&s_dot, r);
         for (int w = 0; w < 32; ++w) n += s_tok[w];
-        *a.valid_tokens = n;
-        const double nn = static_cast<double>(n);
-        *a.loss = n == 0 ? 0.0f
-                         : static_cast<float>(static_cast<double>(a.coef) * a.experts * d / (nn * nn * a.topk));
+        write_loss(a, d, n);
     }
     cluster.sync();         // the other blocks' sums stay until they are read
 }
@@ -323,7 +347,9 @@ cudaError_t launch_shape(const BalanceArgs &a, bool backward, cudaStream_t strea
             <<<static_cast<unsigned>(need < most ? need : most), kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    const int blocks = static_cast<int>(need < kBalanceBlocks ? need : kBalanceBlocks);
+    // four blocks' worth of tokens or fewer: one block and no second kernel
+    // (512 tokens, 8 experts: 31 -> 29 us for both passes, launches included)
+    const int blocks = need <= 4 ? 1 : static_cast<int>(need < kBalanceBlocks ? need : kBalanceBlocks);
     const int smem = a.experts * 4 * (1 + kWarps);
     static std::atomic<uint64_t> done{0};
     if (smem > 48 * 1024 - 256) {
@@ -332,7 +358,7 @@ cudaError_t launch_shape(const BalanceArgs &a, bool backward, cudaStream_t strea
     }
     balance_partial_kernel<G, J, V, BF16><<<blocks, kThreads, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || blocks == 1) return e;
     const int share = (a.experts + kFinishBlocks - 1) / kFinishBlocks;
     int width = 1;
     while (width < share) width *= 2;

@@ -771,26 +771,25 @@ def moe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: tor
 
 def _tensor_table(grads, out):
     """ufp4_tensor_t array of a gradient list (out: destinations, or None)."""
-    table, device = array.array("q"), None
+    _need(len(grads) > 0, "grads: at least one tensor")
+    table, device = [], _device(grads[0])
     for i, t in enumerate(grads):
         o = t if out is None else out[i]
-        if device is None:
-            device = _device(t)
         if t.device != device or o.device != device:
             _device(grads[0], t, o)
-        if not (t.is_contiguous() and o.is_contiguous()) or t.numel() != o.numel():
+        n = t.numel()
+        if not (t.is_contiguous() and o.is_contiguous()) or o.numel() != n:
             raise ValueError(f"gradient {i}: contiguous tensors, a destination of the same size")
-        table.extend((t.data_ptr(), o.data_ptr(), t.numel(), _dtype(t, "gradient") | _dtype(o, "out") << 32))
-    return table, device
+        table += (t.data_ptr(), o.data_ptr(), n, _dtype(t, "gradient") | _dtype(o, "out") << 32)
+    return array.array("q", table), device
 
 
 def grad_norm(grads) -> torch.Tensor:
     """Global norm of a list of gradients (bfloat16 or float32, contiguous):
     float32 [1] on their device."""
     table, device = _tensor_table(grads, None)
-    _need(device is not None, "grads: at least one tensor")
-    norm = torch.empty(1, dtype=torch.float32, device=device)
-    work = torch.empty(lib().ufp4_grad_norm_workspace(len(grads)), dtype=torch.uint8, device=device)
+    norm = grads[0].new_empty(1, dtype=torch.float32)
+    work = norm.new_empty(lib().ufp4_grad_norm_workspace(len(grads)), dtype=torch.uint8)
     _call("ufp4_grad_norm", device, table.buffer_info()[0], len(grads), norm.data_ptr(), work.data_ptr())
     return norm
 
@@ -802,9 +801,8 @@ def grad_clip(grads, max_norm: float, out=None) -> torch.Tensor:
     as they are."""
     _need(out is None or len(out) == len(grads), "out: a tensor for each gradient")
     table, device = _tensor_table(grads, out)
-    _need(device is not None, "grads: at least one tensor")
-    norm = torch.empty(1, dtype=torch.float32, device=device)
-    work = torch.empty(lib().ufp4_grad_norm_workspace(len(grads)), dtype=torch.uint8, device=device)
+    norm = grads[0].new_empty(1, dtype=torch.float32)
+    work = norm.new_empty(lib().ufp4_grad_norm_workspace(len(grads)), dtype=torch.uint8)
     _call("ufp4_grad_clip", device, table.buffer_info()[0], len(grads), max_norm, norm.data_ptr(), work.data_ptr())
     return norm
 
