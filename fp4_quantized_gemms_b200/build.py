@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libufp4.so")
 BUILD_DIR = os.path.join(PKG, "_build")
-SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "diag.cu", "epilogue.cu", "norm.cu", "router.cu", "clip.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "gemm_epilogue.cu", "gemm_epilogue_mx.cu", "diag.cu",
+           "epilogue.cu", "norm.cu", "router.cu", "clip.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -23,6 +23,8 @@ namespace ufp4 {
 cudaError_t read_and_clear_error_word(uint32_t *out);            // gemm.cu
 cudaError_t quantize_read_and_clear_error_word(uint32_t *out);   // quantize.cu
 cudaError_t norm_read_and_clear_error_word(uint32_t *out);       // norm.cu
+cudaError_t gemm_epilogue_read_and_clear_error_word(uint32_t *out);
+cudaError_t gemm_epilogue_mx_read_and_clear_error_word(uint32_t *out);
 cudaError_t quantize_set_producer_wait_limit(uint64_t limit_ns);  // quantize.cu
 
 namespace {
@@ -205,13 +207,15 @@ ufp4_status_t encode_operand_maps(const ufp4_qtensor_t *q, int code_rows, int sc
 // piece of the output, where the residual of the same type arrives first, and
 // one of the stored pre-activation.  So all are bf16, or the output (and the
 // residual) fp32 without a stored pre-activation; and bulk copies need
-// 16-byte aligned rows.  Everything else takes the kernels' element-wise path.
+// 16-byte aligned rows, of whole 16-byte units (a bulk store clips at the
+// unit: the rest of a row's last unit would be written too).  Everything else
+// takes the kernels' element-wise path.
 ufp4_status_t encode_epilogue_maps(GemmArgs *args, int mode, int64_t m, int64_t n) {
     EpiArgs &e = args->epi;
     auto fits = [m](const void *p, int64_t ld, bool bf16) {
         return aligned16(p) && (m == 1 || ld * (bf16 ? 2 : 4) % 16 == 0) && ld < (int64_t(1) << 36);
     };
-    e.tma = mode >= 5 && fits(e.out, e.ld_out, e.out_bf16) &&
+    e.tma = mode >= 5 && n * (e.out_bf16 ? 2 : 4) % 16 == 0 && fits(e.out, e.ld_out, e.out_bf16) &&
             (e.residual == nullptr || (fits(e.residual, e.ld_res, e.res_bf16) && e.res_bf16 == e.out_bf16)) &&
             (e.pre == nullptr || (fits(e.pre, e.ld_pre, e.pre_bf16) && e.pre_bf16 && e.out_bf16));
     if (!e.tma) return UFP4_OK;
@@ -222,10 +226,10 @@ ufp4_status_t encode_epilogue_maps(GemmArgs *args, int mode, int64_t m, int64_t 
                                     bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
     };
     // (a single row may have any pitch; the map wants one that covers a row)
-    auto pitch = [&](int64_t ld, bool bf16) { return m > 1 ? ld : round_up(n, bf16 ? 8 : 4); };
-    if (!encode(&args->tm_out, e.out, pitch(e.ld_out, e.out_bf16), e.out_bf16) ||
-        (e.residual != nullptr && !encode(&args->tm_res, e.residual, pitch(e.ld_res, e.res_bf16), e.res_bf16)) ||
-        (e.pre != nullptr && !encode(&args->tm_pre, e.pre, pitch(e.ld_pre, true), true)))
+    auto pitch = [&](int64_t ld) { return m > 1 ? ld : n; };
+    if (!encode(&args->tm_out, e.out, pitch(e.ld_out), e.out_bf16) ||
+        (e.residual != nullptr && !encode(&args->tm_res, e.residual, pitch(e.ld_res), e.res_bf16)) ||
+        (e.pre != nullptr && !encode(&args->tm_pre, e.pre, pitch(e.ld_pre), true)))
         return UFP4_ERR_CUDA;
     return UFP4_OK;
 }
@@ -1186,11 +1190,12 @@ ufp4_status_t ufp4_test_set_quantize_wait_limit(uint64_t limit_ns) {
 ufp4_status_t ufp4_check_device_status(void) {
     uint32_t w = 0;
     if (read_and_clear_error_word(&w) != cudaSuccess) return UFP4_ERR_CUDA;
-    uint32_t wq = 0;
-    if (quantize_read_and_clear_error_word(&wq) != cudaSuccess) return UFP4_ERR_CUDA;
-    w |= wq;
-    if (norm_read_and_clear_error_word(&wq) != cudaSuccess) return UFP4_ERR_CUDA;
-    w |= wq;
+    for (auto *read : {quantize_read_and_clear_error_word, norm_read_and_clear_error_word,
+                       gemm_epilogue_read_and_clear_error_word, gemm_epilogue_mx_read_and_clear_error_word}) {
+        uint32_t wq = 0;
+        if (read(&wq) != cudaSuccess) return UFP4_ERR_CUDA;
+        w |= wq;
+    }
     return w == 0 ? UFP4_OK : UFP4_ERR_DEVICE_TIMEOUT;
 }
 

@@ -47,13 +47,12 @@ __device__ __forceinline__ void store8(void *p, int64_t i, const float2 (&v)[4])
 }
 
 // Sums of a warp row of columns over the block's warps, written to the
-// chunk's partial row.  Column of (lane, j): 8 lane + j, or lane + 32 j.
-template <bool VEC>
+// chunk's partial row.
 __device__ __forceinline__ void store_partial(const EpiBwdArgs &a, const float (&sum)[8], int64_t col0) {
     __shared__ float s_sum[kBwdWarps][kBwdCols];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s_sum[warp][VEC ? 8 * lane + j : lane + 32 * j] = sum[j];
+    for (int j = 0; j < 8; ++j) s_sum[warp][8 * lane + j] = sum[j];
     __syncthreads();
     const int64_t col = col0 + threadIdx.x;
     if (col < a.n) {
@@ -108,39 +107,64 @@ __global__ void __launch_bounds__(kBwdThreads, 3) epilogue_backward_kernel(const
         }
     }
     const float sums[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
-    if (a.dbias != nullptr) store_partial<true>(a, sums, col0);
+    if (a.dbias != nullptr) store_partial(a, sums, col0);
 }
 
-// Any width, row pitch and alignment: one element per access, a warp's 32
-// lanes side by side.
+// Any width, row pitch and alignment (16384 x 8191: 666 us with one element per
+// access).
 template <int ACT>
-__global__ void __launch_bounds__(kBwdThreads) epilogue_backward_any_kernel(const __grid_constant__ EpiBwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, 2) epilogue_backward_any_kernel(const __grid_constant__ EpiBwdArgs a) {
     let_next_kernel_launch();
+    constexpr int U = 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kBwdCols;
+    const int64_t col = col0 + 8 * lane;
+    const int64_t left = a.n - col;
+    const int rest = left > 1024 ? 1024 : left < -8 ? -8 : static_cast<int>(left);
     const int64_t r_first = blockIdx.y * a.rows_per_chunk + warp;
     const int64_t r_end = min(a.m, (blockIdx.y + 1) * a.rows_per_chunk);
     float sum[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-    for (int64_t r = r_first; r < r_end; r += kBwdWarps) {
-        float d[8], z[8];
+    for (int64_t r0 = r_first; r0 < r_end; r0 += kBwdWarps * U) {     // whole warps
+        float d[U][8], z[U][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t col = col0 + lane + 32 * j;
-            const bool ok = col < a.n;
-            d[j] = ok ? load_elem(a.dout, r * a.ld_dout + col, a.dout_bf16) : 0.0f;
-            if constexpr (ACT != UFP4_ACT_NONE) z[j] = ok ? load_elem(a.pre, r * a.ld_pre + col, a.pre_bf16) : 0.0f;
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + kBwdWarps * u;
+            const int valid = r < r_end ? rest : 0;
+            if (a.dout_bf16)
+                load8_any<true>(a.dout, r * a.ld_dout + col, valid, d[u]);
+            else
+                load8_any<false>(a.dout, r * a.ld_dout + col, valid, d[u]);
+            if constexpr (ACT != UFP4_ACT_NONE) {
+                if (a.pre_bf16)
+                    load8_any<true>(a.pre, r * a.ld_pre + col, valid, z[u]);
+                else
+                    load8_any<false>(a.pre, r * a.ld_pre + col, valid, z[u]);
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t col = col0 + lane + 32 * j;
-            if constexpr (ACT != UFP4_ACT_NONE) d[j] *= act_slope2<ACT>(splat(z[j])).x;
-            sum[j] += d[j];
-            if (a.dpre != nullptr && col < a.n) store_elem(a.dpre, r * a.ld_dpre + col, a.dpre_bf16, d[j]);
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + kBwdWarps * u;
+            if constexpr (ACT != UFP4_ACT_NONE) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 q = mul2(make_float2(d[u][j], d[u][j + 1]), act_slope2<ACT>(make_float2(z[u][j], z[u][j + 1])));
+                    d[u][j] = q.x;
+                    d[u][j + 1] = q.y;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += d[u][j];
+            if (a.dpre != nullptr && r < r_end) {
+                if (a.dpre_bf16)
+                    store8_any<true>(a.dpre, r * a.ld_dpre + col, rest, d[u]);
+                else
+                    store8_any<false>(a.dpre, r * a.ld_dpre + col, rest, d[u]);
+            }
         }
     }
-    if (a.dbias != nullptr) store_partial<false>(a, sum, col0);
+    if (a.dbias != nullptr) store_partial(a, sum, col0);
 }
 
 // out[c] = sum of the partial rows: 32 columns per block, its 32 warps take

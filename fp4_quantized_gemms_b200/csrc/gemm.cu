@@ -34,15 +34,25 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #define UFP4_PIPELINE_KERNELS 1
 #include "ufp4_device.cuh"
 #include "ufp4_elem.cuh"
 #include "ufp4_internal.h"
 
+// This file is compiled three times, side by side: as itself (the kernels that
+// store C), and from gemm_epilogue.cu and gemm_epilogue_mx.cu, which define
+// UFP4_EPILOGUE_PART, for the same kernels with an epilogue.
+#ifndef UFP4_EPILOGUE_PART
+#define UFP4_EPILOGUE_PART 0      // 1: FP4 and fp32-scale kernels, 2: MX kernels
+#endif
+
 namespace ufp4 {
 
 namespace {
+
+constexpr bool kEpilogue = UFP4_EPILOGUE_PART != 0;
 
 constexpr int BM = 128;
 constexpr int BK = 64;             // K elements per pipeline stage
@@ -1349,7 +1359,8 @@ __device__ __forceinline__ void store_piece(const GemmArgs &args, const Tile &tl
 // leaves through the warp's 4 KB buffer by one bulk tensor store, and the
 // residual arrives there by a bulk tensor load that was issued a piece (for
 // the first piece: a tile) earlier; each thread adds its row and overwrites it
-// with the result.  The copies clip rows and columns outside the matrix.  A
+// with the result.  The copies clip rows and columns outside the matrix (rows
+// are whole 16-byte units, which is where a store clips).  A
 // first form finished four columns of eight rows per lane with ordinary
 // accesses: 20 instructions per element against 11, and 298 against 170 us
 // for the MX product 8192 x 8192 x 2048 with GELU, bias and pre-activation.
@@ -1364,8 +1375,6 @@ struct EpiWarp {
     uint32_t phase;        // bit s: parity of slot s's next wait
     uint32_t pending;      // bit s: a residual load into slot s is in flight
 };
-
-__device__ __forceinline__ bool epi_two_slots(const EpiArgs &e) { return e.out_bf16 && e.pre == nullptr; }
 
 // Starts the residual load of the piece at (col, row) into a slot that no
 // store reads any more.
@@ -1407,7 +1416,7 @@ __device__ __forceinline__ bool epilogue_pieces(const GemmArgs &args, EpiWarp &w
                                                 int64_t row0, int64_t col0, int64_t n, uint32_t (&r)[NP][32], float mult,
                                                 volatile uint32_t *abort_flag) {
     const EpiArgs &e = args.epi;
-    const bool res = e.residual != nullptr, two = epi_two_slots(e);
+    const bool res = e.residual != nullptr, two = e.out_bf16 && e.pre == nullptr;
 #pragma unroll
     for (int c = 0; c < NP; ++c) {
         const int64_t col = col0 + 32 * c;
@@ -1507,28 +1516,139 @@ __device__ __forceinline__ bool epilogue_rows(const GemmArgs &args, EpiWarp &w, 
     }
 }
 
-// Any types, pitches and alignments: a piece is transposed through the buffer
-// as fp32, and a lane finishes four columns of a row at a time.
-__device__ __forceinline__ void stage_piece(uint8_t *buf, int lane, const uint32_t (&r)[32], float mult) {
+// 32 columns of a thread's row, fp32, to the buffer.
+__device__ __forceinline__ void epi_stage_f32(uint8_t *buf, int lane, const float (&v)[32]) {
     uint8_t *rowp = buf + lane * 128;
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch)
-        *reinterpret_cast<float4 *>(rowp + ((ch ^ (lane & 7)) << 4)) =
-            make_float4(__fmul_rn(__uint_as_float(r[4 * ch]), mult), __fmul_rn(__uint_as_float(r[4 * ch + 1]), mult),
-                        __fmul_rn(__uint_as_float(r[4 * ch + 2]), mult),
-                        __fmul_rn(__uint_as_float(r[4 * ch + 3]), mult));
+    for (int u = 0; u < 8; ++u)
+        *reinterpret_cast<float4 *>(rowp + ((u ^ (lane & 7)) << 4)) =
+            make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
 }
 
-__device__ __forceinline__ void epilogue_piece_any(const EpiArgs &e, const uint8_t *buf, int lane, int64_t m0,
-                                                   int64_t col0, int64_t m, int64_t n) {
-    const int64_t gcol = col0 + 4 * (lane & 7);
-    const int valid = gcol + 4 <= n ? 4 : static_cast<int>(n - gcol);   // <= 0: outside
-    const float4 bias = epilogue_bias(e, gcol, valid);
+// Byte of column c of row r in a staged piece.
+template <bool BF16>
+__device__ __forceinline__ int epi_byte(int r, int c) {
+    return BF16 ? r * 64 + ((((c >> 3) ^ (r >> 1)) & 3) << 4) + 2 * (c & 7)
+                : r * 128 + (((c >> 2) ^ (r & 7)) << 4) + 4 * (c & 3);
+}
+
+// A staged piece to (or from) the matrix, a row of 32 neighbouring elements per
+// access: any pitch and alignment.
+template <bool BF16, bool OUT>
+__device__ __forceinline__ void epi_copy(void *p, int64_t ld, uint8_t *buf, int lane, int64_t row0, int rows, int64_t col,
+                                         bool col_ok) {
+    using T = std::conditional_t<BF16, uint16_t, uint32_t>;
+    constexpr int U = OUT ? 4 : 16;                   // loads: two round trips per piece
+    T *g = static_cast<T *>(p) + row0 * ld + col + lane;
+    if (!col_ok) return;
 #pragma unroll 1
-    for (int rr = lane >> 3; rr < 32; rr += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-        if (m0 + rr < m && valid > 0)
-            epilogue_quad(e, m0 + rr, gcol, valid, v, bias, epilogue_residual(e, m0 + rr, gcol, valid));
+    for (int r0 = 0; r0 < rows; r0 += U) {
+        T v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if constexpr (OUT)
+                v[k] = *reinterpret_cast<const T *>(buf + epi_byte<BF16>(r0 + k, lane));
+            else
+                v[k] = r0 + k < rows ? g[k * ld] : T(0);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if constexpr (OUT) {
+                if (r0 + k < rows) g[k * ld] = v[k];
+            } else {
+                *reinterpret_cast<T *>(buf + epi_byte<BF16>(r0 + k, lane)) = v[k];
+            }
+        }
+        g += U * ld;
+    }
+}
+
+// Stages 32 columns of a thread's row and writes the warp's piece out.
+__device__ __forceinline__ void epi_put(void *p, int64_t ld, bool bf16, uint8_t *buf, int lane, int64_t row0, int rows,
+                                        int64_t col, bool col_ok, const float (&v)[32]) {
+    __syncwarp();
+    if (bf16) {
+        epi_stage_bf16(buf, lane, v);
+        __syncwarp();
+        epi_copy<true, true>(p, ld, buf, lane, row0, rows, col, col_ok);
+    } else {
+        epi_stage_f32(buf, lane, v);
+        __syncwarp();
+        epi_copy<false, true>(p, ld, buf, lane, row0, rows, col, col_ok);
+    }
+}
+
+// The pieces of a warp for any types, pitches and alignments: the same
+// arithmetic on rows, with pre, residual and out in turn through the whole
+// buffer by ordinary accesses (MX 8192 x 8191 x 2048 with GELU and bias: 190
+// us; finishing columns of a staged piece, with each element's address and
+// type on the way, took 400).  The four pieces are unrolled: with one copy of
+// this code the 128 accumulators live across it spilled, and the kernel's
+// shared memory leaves too little L1 for that (313 us).
+template <int ACT>
+__device__ __forceinline__ void epilogue_pieces_any(const EpiArgs &e, uint8_t *buf, int lane, const float *bias,
+                                                    int64_t row0, int64_t col0, int64_t m, int64_t n,
+                                                    const uint32_t (&r)[4][32], float mult) {
+    const int rows = m - row0 < 32 ? static_cast<int>(m - row0) : 32;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int64_t col = col0 + 32 * c;
+        if (col >= n) break;                          // the same for the whole warp
+        const bool col_ok = col + lane < n;
+        float v[32];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 b = *reinterpret_cast<const float4 *>(bias + 32 * c + 4 * q);
+            v[4 * q] = fmaf(__uint_as_float(r[c][4 * q]), mult, b.x);
+            v[4 * q + 1] = fmaf(__uint_as_float(r[c][4 * q + 1]), mult, b.y);
+            v[4 * q + 2] = fmaf(__uint_as_float(r[c][4 * q + 2]), mult, b.z);
+            v[4 * q + 3] = fmaf(__uint_as_float(r[c][4 * q + 3]), mult, b.w);
+        }
+        if (e.pre != nullptr) epi_put(e.pre, e.ld_pre, e.pre_bf16, buf, lane, row0, rows, col, col_ok, v);
+        if constexpr (ACT != UFP4_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], ACT);
+        }
+        if (e.residual != nullptr) {
+            __syncwarp();
+            if (e.res_bf16) {
+                epi_copy<true, false>(const_cast<void *>(e.residual), e.ld_res, buf, lane, row0, rows, col, col_ok);
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(buf + epi_byte<true>(lane, 8 * u));
+                    const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[8 * u + 2 * k] += bf16_lo(qw[k]);
+                        v[8 * u + 2 * k + 1] += bf16_hi(qw[k]);
+                    }
+                }
+            } else {
+                epi_copy<false, false>(const_cast<void *>(e.residual), e.ld_res, buf, lane, row0, rows, col, col_ok);
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float4 q = *reinterpret_cast<const float4 *>(buf + epi_byte<false>(lane, 4 * u));
+                    v[4 * u] += q.x, v[4 * u + 1] += q.y, v[4 * u + 2] += q.z, v[4 * u + 3] += q.w;
+                }
+            }
+        }
+        epi_put(e.out, e.ld_out, e.out_bf16, buf, lane, row0, rows, col, col_ok, v);
+    }
+    __syncwarp();                                     // buffer read out
+}
+
+__device__ __forceinline__ void epilogue_rows_any(const EpiArgs &e, uint8_t *buf, int lane, const float *bias, int64_t row0,
+                                                  int64_t col0, int64_t m, int64_t n, const uint32_t (&r)[4][32], float mult) {
+    switch (e.act) {
+        case UFP4_ACT_RELU: epilogue_pieces_any<UFP4_ACT_RELU>(e, buf, lane, bias, row0, col0, m, n, r, mult); break;
+        case UFP4_ACT_GELU: epilogue_pieces_any<UFP4_ACT_GELU>(e, buf, lane, bias, row0, col0, m, n, r, mult); break;
+        case UFP4_ACT_GELU_ERF:
+            epilogue_pieces_any<UFP4_ACT_GELU_ERF>(e, buf, lane, bias, row0, col0, m, n, r, mult);
+            break;
+        case UFP4_ACT_SILU: epilogue_pieces_any<UFP4_ACT_SILU>(e, buf, lane, bias, row0, col0, m, n, r, mult); break;
+        default: epilogue_pieces_any<UFP4_ACT_NONE>(e, buf, lane, bias, row0, col0, m, n, r, mult); break;
     }
 }
 
@@ -1894,16 +2014,14 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
             // emptied it).  The first residual piece starts its way now.
             float *bias_s = reinterpret_cast<float *>(smem + C::o_bias) + 256 * (tcount & 1);
             if constexpr (EPI) {
-                if (args.epi.tma) {
 #pragma unroll
-                    for (int hh = 0; hh < kHalves; ++hh) {
-                        const int col = 128 * (h0 + hh) + 4 * lane;
-                        const int64_t left = tl.g.n - (tl.n0 + col);
-                        const int valid = left < 0 ? 0 : left < 4 ? static_cast<int>(left) : 4;
-                        *reinterpret_cast<float4 *>(bias_s + col) = epilogue_bias(args.epi, tl.n0 + col, valid);
-                    }
-                    __syncwarp();
+                for (int hh = 0; hh < kHalves; ++hh) {
+                    const int col = 128 * (h0 + hh) + 4 * lane;
+                    const int64_t left = tl.g.n - (tl.n0 + col);
+                    const int valid = left < 0 ? 0 : left < 4 ? static_cast<int>(left) : 4;
+                    *reinterpret_cast<float4 *>(bias_s + col) = epilogue_bias(args.epi, tl.n0 + col, valid);
                 }
+                __syncwarp();
             }
             if (EPI && args.epi.tma && args.epi.residual != nullptr && m0 < tl.g.m && tl.n0 + 128 * h0 < tl.g.n) {
                 if (lane == 0) bulk_wait_read<0>();
@@ -1913,7 +2031,8 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
             tc_fence_after();
             const bool vec_tile = args.c_vec && (tl.g.c_col & 3) == 0;
             const bool zero = tl.g.k == 0;             // no MMA wrote the accumulator
-#pragma unroll
+            constexpr int kUnroll = EPI ? 1 : kHalves;     // (the epilogue's code is long)
+#pragma unroll kUnroll
             for (int hh = 0; hh < kHalves; ++hh) {
                 const int h = h0 + hh;
                 if (EPI && hh > 0 && args.epi.tma && args.epi.residual != nullptr && m0 < tl.g.m &&
@@ -1941,20 +2060,9 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
                                                   abort_flag);
                         continue;
                     }
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        const int64_t col0 = tl.n0 + 128 * h + 32 * c;
-                        if (col0 >= tl.g.n) break;        // the same for the whole warp
-                        switch (c) {                      // one copy of the finishing code for the four pieces
-                            case 0: stage_piece(buf, lane, r[0], mult); break;
-                            case 1: stage_piece(buf, lane, r[1], mult); break;
-                            case 2: stage_piece(buf, lane, r[2], mult); break;
-                            default: stage_piece(buf, lane, r[3], mult); break;
-                        }
-                        __syncwarp();
-                        epilogue_piece_any(args.epi, buf, lane, m0, col0, tl.g.m, tl.g.n);
-                        __syncwarp();                     // buffer read out before the next piece
-                    }
+if (m0 < tl.g.m)
+                        epilogue_rows_any(args.epi, buf, lane, bias_s + 128 * h, m0, tl.n0 + 128 * h, tl.g.m, tl.g.n, r,
+                                          mult);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -1977,11 +2085,11 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
     }
 }
 
-template <int GRID, bool ATOMS, bool LANES, bool EPI>
-cudaError_t launch_pair_epi(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+template <int GRID, bool ATOMS, bool LANES = false>
+cudaError_t launch_pair(const GemmArgs &args, int num_sms, cudaStream_t stream) {
     using C = PairCfg<GRID, ATOMS, LANES>;
     static std::atomic<uint64_t> configured{0};
-    const cudaError_t ce = allow_smem(gemm_pair_kernel<GRID, ATOMS, LANES, EPI>, C::kAlloc, configured);
+    const cudaError_t ce = allow_smem(gemm_pair_kernel<GRID, ATOMS, LANES, kEpilogue>, C::kAlloc, configured);
     if (ce != cudaSuccess) return ce;
     int units = num_sms / 2;
     if (args.groups == nullptr) {
@@ -2002,20 +2110,14 @@ cudaError_t launch_pair_epi(const GemmArgs &args, int num_sms, cudaStream_t stre
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<GRID, ATOMS, LANES, EPI>, args);
+    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<GRID, ATOMS, LANES, kEpilogue>, args);
 }
 
-template <int GRID, bool ATOMS, bool LANES = false>
-cudaError_t launch_pair(const GemmArgs &args, int num_sms, cudaStream_t stream) {
-    return args.epilogue ? launch_pair_epi<GRID, ATOMS, LANES, true>(args, num_sms, stream)
-                         : launch_pair_epi<GRID, ATOMS, LANES, false>(args, num_sms, stream);
-}
-
-template <int GRID, bool CIN, bool EPI>
-cudaError_t launch_fp4_epi(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+template <int GRID, bool CIN>
+cudaError_t launch_fp4(const GemmArgs &args, int num_sms, cudaStream_t stream) {
     using C = Fp4Cfg<GRID, CIN>;
     static std::atomic<uint64_t> configured{0};
-    const cudaError_t ce = allow_smem(gemm_fp4_kernel<GRID, CIN, EPI>, C::kAlloc, configured);
+    const cudaError_t ce = allow_smem(gemm_fp4_kernel<GRID, CIN, kEpilogue>, C::kAlloc, configured);
     if (ce != cudaSuccess) return ce;
     int units = num_sms;
     if (args.groups == nullptr) {
@@ -2024,21 +2126,15 @@ cudaError_t launch_fp4_epi(const GemmArgs &args, int num_sms, cudaStream_t strea
         if (tiles < units) units = static_cast<int>(tiles);
     }
     if (units <= 0) return cudaSuccess;
-    gemm_fp4_kernel<GRID, CIN, EPI><<<units, C::kThreads, C::kAlloc, stream>>>(args);
+    gemm_fp4_kernel<GRID, CIN, kEpilogue><<<units, C::kThreads, C::kAlloc, stream>>>(args);
     return cudaGetLastError();
 }
 
-template <int GRID, bool CIN>
-cudaError_t launch_fp4(const GemmArgs &args, int num_sms, cudaStream_t stream) {
-    return args.epilogue ? launch_fp4_epi<GRID, CIN, true>(args, num_sms, stream)
-                         : launch_fp4_epi<GRID, CIN, false>(args, num_sms, stream);
-}
-
-template <int GRID, bool UE8, bool EPI>
-cudaError_t launch_f32s_epi(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+template <int GRID, bool UE8>
+cudaError_t launch_f32s_fmt(const GemmArgs &args, int num_sms, cudaStream_t stream) {
     using C = F32sCfg;
     static std::atomic<uint64_t> configured{0};
-    const cudaError_t ce = allow_smem(gemm_f32s_kernel<GRID, UE8, EPI>, C::kAlloc, configured);
+    const cudaError_t ce = allow_smem(gemm_f32s_kernel<GRID, UE8, kEpilogue>, C::kAlloc, configured);
     if (ce != cudaSuccess) return ce;
     int units = num_sms;
     if (args.groups == nullptr) {
@@ -2047,15 +2143,10 @@ cudaError_t launch_f32s_epi(const GemmArgs &args, int num_sms, cudaStream_t stre
         if (tiles < units) units = static_cast<int>(tiles);
     }
     if (units <= 0) return cudaSuccess;
-    gemm_f32s_kernel<GRID, UE8, EPI><<<units, C::kThreads, C::kAlloc, stream>>>(args);
+    gemm_f32s_kernel<GRID, UE8, kEpilogue><<<units, C::kThreads, C::kAlloc, stream>>>(args);
     return cudaGetLastError();
 }
 
-template <int GRID, bool UE8>
-cudaError_t launch_f32s_fmt(const GemmArgs &args, int num_sms, cudaStream_t stream) {
-    return args.epilogue ? launch_f32s_epi<GRID, UE8, true>(args, num_sms, stream)
-                         : launch_f32s_epi<GRID, UE8, false>(args, num_sms, stream);
-}
 
 // fp32 or UE8M0 block scales: the scale decode is a compile-time choice.
 template <int GRID>
@@ -2064,11 +2155,35 @@ cudaError_t launch_f32s(const GemmArgs &args, int num_sms, cudaStream_t stream) 
                             : launch_f32s_fmt<GRID, false>(args, num_sms, stream);
 }
 
+// Reads and clears this translation unit's error word.
+cudaError_t clear_error_word(uint32_t *out) {
+    const cudaError_t e = cudaMemcpyFromSymbol(out, g_error_word, sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    const uint32_t zero = 0;
+    return cudaMemcpyToSymbol(g_error_word, &zero, sizeof(uint32_t));
+}
+
 }  // namespace
 
+#if UFP4_EPILOGUE_PART == 2
+cudaError_t launch_gemm_epilogue_mx(const GemmArgs &args, int num_sms, cudaStream_t stream) {
+    return args.atoms ? launch_pair<3, true>(args, num_sms, stream) : launch_pair<3, false>(args, num_sms, stream);
+}
+
+cudaError_t gemm_epilogue_mx_read_and_clear_error_word(uint32_t *out) { return clear_error_word(out); }
+#else
+#if UFP4_EPILOGUE_PART == 1
+cudaError_t launch_gemm_epilogue(const GemmArgs &args, int mode, int grid_kind, int num_sms, cudaStream_t stream) {
+    switch (mode) {
+        case 6: return launch_gemm_epilogue_mx(args, num_sms, stream);
+#else
 cudaError_t launch_gemm(const GemmArgs &args, int mode, int grid_kind, int num_sms,
                         cudaStream_t stream) {
+    if (args.epilogue) return launch_gemm_epilogue(args, mode, grid_kind, num_sms, stream);
     switch (mode) {
+        case 6:
+            return args.atoms ? launch_pair<3, true>(args, num_sms, stream) : launch_pair<3, false>(args, num_sms, stream);
+#endif
         case 0:
             return grid_kind == 0 ? launch_f32s<0>(args, num_sms, stream) : launch_f32s<1>(args, num_sms, stream);
         case 3:
@@ -2081,26 +2196,20 @@ cudaError_t launch_gemm(const GemmArgs &args, int mode, int grid_kind, int num_s
                                                     : launch_pair<0, true, false>(args, num_sms, stream));
             return grid_kind == 1 ? launch_pair<1, false>(args, num_sms, stream)
                                   : launch_pair<0, false>(args, num_sms, stream);
-        case 6:
-            return args.atoms ? launch_pair<3, true>(args, num_sms, stream) : launch_pair<3, false>(args, num_sms, stream);
         default:
             return cudaErrorInvalidValue;
     }
 }
 
-}  // namespace ufp4
-
-namespace ufp4 {
-
-// Host side of ufp4_check_device_status (the error word lives in this
-// translation unit).  Synchronises the current device.
+#if UFP4_EPILOGUE_PART == 1
+cudaError_t gemm_epilogue_read_and_clear_error_word(uint32_t *out) { return clear_error_word(out); }
+#else
+// Host side of ufp4_check_device_status.  Synchronises the current device.
 cudaError_t read_and_clear_error_word(uint32_t *out) {
-    cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyFromSymbol(out, g_error_word, sizeof(uint32_t));
-    if (e != cudaSuccess) return e;
-    const uint32_t zero = 0;
-    return cudaMemcpyToSymbol(g_error_word, &zero, sizeof(uint32_t));
+    const cudaError_t e = cudaDeviceSynchronize();
+    return e != cudaSuccess ? e : clear_error_word(out);
 }
+#endif
+#endif
 
 }  // namespace ufp4

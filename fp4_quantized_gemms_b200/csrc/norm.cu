@@ -29,14 +29,15 @@ namespace ufp4 {
 
 namespace {
 
-// Eight consecutive elements starting at p[i]: 16-byte accesses (VEC), or one
-// by one, those at or beyond `valid` read as 0 and left alone.
+// Eight consecutive elements starting at p[i], lane l's behind lane l - 1's;
+// `rest`: elements of the row from there on (any number; those beyond it are
+// read as 0 and not written).  VEC: rows are 16-byte aligned and a multiple of
+// eight long.
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int valid, float (&v)[8]) {
+__device__ __forceinline__ void load8(const void *p, int64_t i, int rest, float (&v)[8]) {
     if constexpr (!VEC) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < valid ? load_elem(p, i + j, BF16) : 0.0f;
-    } else if (valid <= 0) {
+        load8_any<BF16>(p, i, rest, v);
+    } else if (rest <= 0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
     } else if constexpr (BF16) {
@@ -56,12 +57,10 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, int valid, float
 }
 
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void put8(void *p, int64_t i, int valid, const float (&v)[8]) {
+__device__ __forceinline__ void put8(void *p, int64_t i, int rest, const float (&v)[8]) {
     if constexpr (!VEC) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < valid) store_elem(p, i + j, BF16, v[j]);
-    } else if (valid > 0) {
+        store8_any<BF16>(p, i, rest, v);                   // all 32 lanes
+    } else if (rest > 0) {
         if constexpr (BF16) {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
                 make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
@@ -73,15 +72,17 @@ __device__ __forceinline__ void put8(void *p, int64_t i, int valid, const float 
     }
 }
 
-__device__ __forceinline__ void load_weight8(const void *w, bool bf16, int64_t i, int valid, bool vec, float (&v)[8]) {
+__device__ __forceinline__ void load_weight8(const void *w, bool bf16, int64_t i, int rest, bool vec, float (&v)[8]) {
     if (vec) {
         if (bf16)
-            load8<true, true>(w, i, valid, v);
+            load8<true, true>(w, i, rest, v);
         else
-            load8<false, true>(w, i, valid, v);
+            load8<false, true>(w, i, rest, v);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < valid ? load_elem(w, i + j, bf16) : 0.0f;
+        if (bf16)
+            load8_any<true>(w, i, rest, v);
+        else
+            load8_any<false>(w, i, rest, v);
     }
 }
 
@@ -163,10 +164,10 @@ struct RowFactors {
 // their blocks' factors (all lanes of the warp take part: a block of 32
 // elements is four neighbouring lanes; elements beyond the row are 0).
 template <bool OUT8, bool VEC>
-__device__ __forceinline__ void write_y(const NormArgs &a, const RowFactors &f, int64_t row, int col, int valid,
+__device__ __forceinline__ void write_y(const NormArgs &a, const RowFactors &f, int64_t row, int col, int rest,
                                         const float (&v)[8]) {
     if constexpr (!OUT8) {
-        put8<true, VEC>(a.y, row * a.ld_y + col, valid, v);
+        put8<true, VEC>(a.y, row * a.ld_y + col, rest, v);
     } else {
         float amax = max_abs3(max_abs3(max_abs3(v[0], v[1], v[2]), v[3], v[4]), max_abs3(v[5], v[6], v[7]), 0.0f);
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
@@ -218,39 +219,53 @@ __device__ __forceinline__ void drain_ring(RingState &s, int64_t from, int64_t t
         mbar_wait(&s.full[k % stages], static_cast<uint32_t>(k / stages) & 1u, kErrTimeoutDrain, &dummy);
 }
 
-// Eight elements of a staged row.
-template <bool BF16>
-__device__ __forceinline__ void load8s(const uint8_t *p, int col, bool ok, float (&v)[8]) {
-    load8<BF16, true>(p, col, ok ? 8 : 0, v);
-}
+// A row of a tensor in a stage: the 16-byte granules that hold it, so with
+// `shift` bytes of something else in front when the row is not aligned.
+template <bool BF16, bool VEC>
+struct StagedRow {
+    const uint8_t *src;        // first granule
+    uint32_t shift, bytes;     // of its first element; of the granules
+    __device__ __forceinline__ StagedRow(const void *base, int64_t row, int64_t ld, int cols) {
+        src = static_cast<const uint8_t *>(base) + row * ld * (BF16 ? 2 : 4);
+        shift = VEC ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
+        src -= shift;
+        bytes = (shift + static_cast<uint32_t>(cols) * (BF16 ? 2u : 4u) + 15u) / 16u * 16u;
+    }
+    // shared memory that a row of the tensor takes at most
+    static __host__ __device__ __forceinline__ uint32_t room(int cols) {
+        return (static_cast<uint32_t>(cols) * (BF16 ? 2u : 4u) + 15u) / 16u * 16u + (VEC ? 0u : 16u);
+    }
+};
 
-template <bool BF16>
-__device__ __forceinline__ void load8s(const uint8_t *p, int col, bool ok, float2 (&v)[4]) {
+// Eight elements of a staged row (at `p`, its shift included) as pairs.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8s(const uint8_t *p, int col, int rest, float2 (&v)[4]) {
     float f[8];
-    load8<BF16, true>(p, col, ok ? 8 : 0, f);
+    load8<BF16, VEC>(p, col, rest, f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
 }
 
-template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8>
+template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8, bool VEC>
 __global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RingState st;
     __shared__ float s_sum[2][W];
     const int t = threadIdx.x;
     const int cols = static_cast<int>(a.cols);
-    const uint32_t x_bytes = static_cast<uint32_t>(cols) * (XBF16 ? 2u : 4u);
-    const uint32_t r_bytes = RES ? static_cast<uint32_t>(cols) * (SBF16 ? 2u : 4u) : 0u;
+    using XRow = StagedRow<XBF16, VEC>;
+    using RRow = StagedRow<SBF16, VEC>;
+    const uint32_t x_room = XRow::room(cols);
     const int64_t n = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;      // rows of this block
     auto issue = [&](int64_t k) {
         const int s = static_cast<int>(k % a.stages);
         const int64_t row = blockIdx.x + k * gridDim.x;
         uint8_t *buf = ring + s * a.stage_bytes;
-        mbar_arrive_expect_tx(&st.full[s], x_bytes + r_bytes);
-        bulk_load(buf, static_cast<const uint8_t *>(a.x) + row * a.ld_x * (XBF16 ? 2 : 4), x_bytes, &st.full[s]);
-        if constexpr (RES)
-            bulk_load(buf + x_bytes, static_cast<const uint8_t *>(a.residual) + row * a.ld_res * (SBF16 ? 2 : 4),
-                      r_bytes, &st.full[s]);
+        const XRow x(a.x, row, a.ld_x, cols);
+        const RRow r(a.residual, row, a.ld_res, cols);
+        mbar_arrive_expect_tx(&st.full[s], x.bytes + (RES ? r.bytes : 0u));
+        bulk_load(buf, x.src, x.bytes, &st.full[s]);
+        if constexpr (RES) bulk_load(buf + x_room, r.src, r.bytes, &st.full[s]);
     };
     if (t == 0) {
         for (int s = 0; s < a.stages; ++s) mbar_init(&st.full[s], 1);
@@ -277,15 +292,16 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_const
     for (; k < n; ++k) {
         const int64_t row = blockIdx.x + k * gridDim.x;
         bad = !mbar_wait(&st.full[s], parity, kErrTimeoutTransform, &st.abort);
-        const uint8_t *buf = ring + s * a.stage_bytes;
+        const uint8_t *x_row = ring + s * a.stage_bytes + XRow(a.x, row, a.ld_x, cols).shift;
+        const uint8_t *r_row = ring + s * a.stage_bytes + x_room + RRow(a.residual, row, a.ld_res, cols).shift;
         float2 h[NV][4], sq = splat(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = 8 * (t + 32 * W * j);
-            load8s<XBF16>(buf, col, col < cols, h[j]);
+            load8s<XBF16, VEC>(x_row, col, cols - col, h[j]);
             if constexpr (RES) {
                 float2 r[4];
-                load8s<SBF16>(buf + x_bytes, col, col < cols, r);
+                load8s<SBF16, VEC>(r_row, col, cols - col, r);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[j][e] = add2(h[j][e], r[e]);
                 if constexpr (SBF16) {                    // the stream as it is stored
@@ -295,13 +311,14 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_const
                         hw[e] = pack_bf16(h[j][e].x, h[j][e].y);
                         h[j][e] = make_float2(bf16_lo(hw[e]), bf16_hi(hw[e]));
                     }
-                    if (col < cols)
+                    if (VEC && col < cols)
                         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.h) + row * a.ld_h + col) =
                             make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                } else if (col < cols) {
-                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.h) + row * a.ld_h + col);
-                    dst[0] = make_float4(h[j][0].x, h[j][0].y, h[j][1].x, h[j][1].y);
-                    dst[1] = make_float4(h[j][2].x, h[j][2].y, h[j][3].x, h[j][3].y);
+                }
+                if constexpr (!SBF16 || !VEC) {
+                    const float hv[8] = {h[j][0].x, h[j][0].y, h[j][1].x, h[j][1].y,
+                                         h[j][2].x, h[j][2].y, h[j][3].x, h[j][3].y};
+                    put8<SBF16, VEC>(a.h, row * a.ld_h + col, cols - col, hv);
                 }
             }
 #pragma unroll
@@ -324,7 +341,7 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_const
                 y[2 * e] = v.x;
                 y[2 * e + 1] = v.y;
             }
-            write_y<OUT8, true>(a, factors, row, col, cols - col, y);
+            write_y<OUT8, VEC>(a, factors, row, col, cols - col, y);
         }
         if (++s == a.stages) {
             s = 0;
@@ -346,17 +363,17 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_kernel(const __
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int64_t col = 8 * (t + S::kRowThreads * j);
-        const int valid = col + 8 <= a.cols ? 8 : static_cast<int>(a.cols - col);
-        load8<XBF16, VEC>(a.x, row * a.ld_x + col, valid, h[j]);
+        const int rest = static_cast<int>(a.cols - col);
+        load8<XBF16, VEC>(a.x, row * a.ld_x + col, rest, h[j]);
         if constexpr (RES) {
             float r[8];
-            load8<SBF16, VEC>(a.residual, row * a.ld_res + col, valid, r);
+            load8<SBF16, VEC>(a.residual, row * a.ld_res + col, rest, r);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 h[j][e] += r[e];
                 if constexpr (SBF16) h[j][e] = __bfloat162float(__float2bfloat16_rn(h[j][e]));
             }
-            put8<SBF16, VEC>(a.h, row * a.ld_h + col, valid, h[j]);
+            put8<SBF16, VEC>(a.h, row * a.ld_h + col, rest, h[j]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(h[j][e], h[j][e], sum);
@@ -368,12 +385,12 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_kernel(const __
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int col = 8 * (t + S::kRowThreads * j);
-        const int valid = col + 8 <= a.cols ? 8 : static_cast<int>(a.cols - col);
+        const int rest = static_cast<int>(a.cols - col);
         float w[8];
-        load_weight8(a.weight, a.weight_bf16, col, valid, a.vec_weight, w);
+        load_weight8(a.weight, a.weight_bf16, col, rest, a.vec_weight, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * rstd * w[e];
-        write_y<OUT8, VEC>(a, factors, row, col, valid, h[j]);
+        write_y<OUT8, VEC>(a, factors, row, col, rest, h[j]);
     }
 }
 
@@ -389,17 +406,14 @@ __device__ __forceinline__ void write_partial(const NormBwdArgs &a, const float 
     }
 }
 
-// Backward: a block takes rows blockIdx.x * R + its row slot, + gridDim.x * R,
-// ..., and keeps the weight gradient of its columns in registers; each block's
-// sums go to its partial row.
+// Backward of rows that do not fit the ring: a block takes rows blockIdx.x, +
+// gridDim.x, ..., and keeps the weight gradient of its columns in registers;
+// its sums go to its partial row.
 template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16, bool VEC>
-__global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel(const __grid_constant__ NormBwdArgs a) {
+__global__ void __launch_bounds__(32 * W) rmsnorm_backward_kernel(const __grid_constant__ NormBwdArgs a) {
     let_next_kernel_launch();
-    using S = RowShape<W>;
     __shared__ float s_sum[2][W];
-    const int t = W == 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * S::kRows + (W == 1 ? threadIdx.x >> 5 : 0);
-    const int64_t nslots = static_cast<int64_t>(gridDim.x) * S::kRows;
+    const int t = threadIdx.x;
     float dw[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -407,18 +421,18 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel
         for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
     int phase = 0;
-    for (int64_t row = slot; row < a.rows; row += nslots, phase ^= 1) {
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, phase ^= 1) {
         const float r = a.rstd[row];
         float xh[NV][8], g[NV][8];
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = 8 * (t + S::kRowThreads * j);
-            const int valid = col + 8 <= a.cols ? 8 : static_cast<int>(a.cols - col);
+            const int64_t col = 8 * (t + 32 * W * j);
+            const int rest = static_cast<int>(a.cols - col);
             float w[8];
-            load8<SBF16, VEC>(a.h, row * a.ld_h + col, valid, xh[j]);
-            load8<DYBF16, VEC>(a.dy, row * a.ld_dy + col, valid, g[j]);
-            load_weight8(a.weight, a.weight_bf16, col, valid, a.vec_weight, w);
+            load8<SBF16, VEC>(a.h, row * a.ld_h + col, rest, xh[j]);
+            load8<DYBF16, VEC>(a.dy, row * a.ld_dy + col, rest, g[j]);
+            load_weight8(a.weight, a.weight_bf16, col, rest, a.vec_weight, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 xh[j][e] *= r;
@@ -431,40 +445,28 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_backward_kernel
         dot = row_sum<W>(dot, s_sum[phase]) * inv_cols;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = 8 * (t + S::kRowThreads * j);
-            const int valid = col + 8 <= a.cols ? 8 : static_cast<int>(a.cols - col);
+            const int64_t col = 8 * (t + 32 * W * j);
+            const int rest = static_cast<int>(a.cols - col);
             float d[8];
             if (a.dh != nullptr) {
-                load8<SBF16, VEC>(a.dh, row * a.ld_dh + col, valid, d);
+                load8<SBF16, VEC>(a.dh, row * a.ld_dh + col, rest, d);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = 0.0f;
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = fmaf(r, g[j][e] - xh[j][e] * dot, d[e]);
-            put8<DXBF16, VEC>(a.dx, row * a.ld_dx + col, valid, d);
+            put8<DXBF16, VEC>(a.dx, row * a.ld_dx + col, rest, d);
         }
     }
-    if (a.dweight == nullptr) return;
-    if constexpr (W == 1) {        // the block's four rows together
-        __shared__ float s_dw[S::kRows][256 * NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s_dw[threadIdx.x >> 5][8 * (t + 32 * j) + e] = dw[j][e];
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.cols; c += S::kThreads)
-            a.partial[blockIdx.x * a.cols + c] = (s_dw[0][c] + s_dw[1][c]) + (s_dw[2][c] + s_dw[3][c]);
-    } else {
-        write_partial<W, NV>(a, dw);
-    }
+    if (a.dweight != nullptr) write_partial<W, NV>(a, dw);
 }
 
-// Backward of short aligned rows: a warp takes U rows at a time (U NV <= 4
+// Backward of short rows: a warp takes U rows at a time (U NV <= 4
 // vectors of each tensor in flight per lane), all loads before the dot
 // product, the elements kept as loaded so that 16 warps fit an SM; the weight
 // is read again for each row (from L1).
-template <int NV, int U, bool SBF16, bool DYBF16, bool DXBF16>
+template <int NV, int U, bool SBF16, bool DYBF16, bool DXBF16, bool VEC>
 __global__ void __launch_bounds__(128, 4) rmsnorm_backward_short_kernel(const __grid_constant__ NormBwdArgs a) {
     let_next_kernel_launch();
     __shared__ float s_dw[4][256 * NV];
@@ -490,13 +492,20 @@ __global__ void __launch_bounds__(128, 4) rmsnorm_backward_short_kernel(const __
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int col = 8 * (lane + 32 * j);
-                h[u][j].zero();
-                g[u][j].zero();
-                d[u][j].zero();
-                if (in && col < cols) {
-                    h[u][j].load(a.h, row * a.ld_h + col);
-                    g[u][j].load(a.dy, row * a.ld_dy + col);
-                    if (has_dh) d[u][j].load(a.dh, row * a.ld_dh + col);
+                if constexpr (VEC) {
+                    h[u][j].zero();
+                    g[u][j].zero();
+                    d[u][j].zero();
+                    if (in && col < cols) {
+                        h[u][j].load(a.h, row * a.ld_h + col);
+                        g[u][j].load(a.dy, row * a.ld_dy + col);
+                        if (has_dh) d[u][j].load(a.dh, row * a.ld_dh + col);
+                    }
+                } else {
+                    const int rest = in ? cols - col : 0;
+                    h[u][j].load_any(a.h, row * a.ld_h + col, rest);
+                    g[u][j].load_any(a.dy, row * a.ld_dy + col, rest);
+                    d[u][j].load_any(a.dh, row * a.ld_dh + col, has_dh ? rest : 0);
                 }
             }
         }
@@ -535,7 +544,7 @@ __global__ void __launch_bounds__(128, 4) rmsnorm_backward_short_kernel(const __
                 d[u][j].get(o);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] = fmaf(r[u], y[e] * w[e] - x[e] * r[u] * dot[u], o[e]);
-                if (row0 + u < a.rows) put8<DXBF16, true>(a.dx, (row0 + u) * a.ld_dx + col, cols - col, o);
+                if (row0 + u < a.rows) put8<DXBF16, VEC>(a.dx, (row0 + u) * a.ld_dx + col, cols - col, o);
             }
         }
     }
@@ -551,7 +560,7 @@ __global__ void __launch_bounds__(128, 4) rmsnorm_backward_short_kernel(const __
 
 // Backward through the ring: h, dy and dh of the next rows are on their way
 // while a row's dot product is reduced.
-template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16>
+template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16, bool VEC>
 __global__ void __launch_bounds__(32 * W) rmsnorm_backward_ring_kernel(const __grid_constant__ NormBwdArgs a) {
     let_next_kernel_launch();
     extern __shared__ __align__(128) uint8_t ring[];
@@ -560,20 +569,20 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_backward_ring_kernel(const __g
     const int t = threadIdx.x;
     const int cols = static_cast<int>(a.cols);
     const bool has_dh = a.dh != nullptr;
-    const uint32_t h_bytes = static_cast<uint32_t>(cols) * (SBF16 ? 2u : 4u);
-    const uint32_t g_bytes = static_cast<uint32_t>(cols) * (DYBF16 ? 2u : 4u);
+    using HRow = StagedRow<SBF16, VEC>;
+    using GRow = StagedRow<DYBF16, VEC>;
+    const uint32_t g_at = HRow::room(cols), d_at = g_at + GRow::room(cols);
     const int64_t n = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
     auto issue = [&](int64_t k) {
         const int s = static_cast<int>(k % a.stages);
         const int64_t row = blockIdx.x + k * gridDim.x;
         uint8_t *buf = ring + s * a.stage_bytes;
-        mbar_arrive_expect_tx(&st.full[s], h_bytes + g_bytes + (has_dh ? h_bytes : 0u));
-        bulk_load(buf, static_cast<const uint8_t *>(a.h) + row * a.ld_h * (SBF16 ? 2 : 4), h_bytes, &st.full[s]);
-        bulk_load(buf + h_bytes, static_cast<const uint8_t *>(a.dy) + row * a.ld_dy * (DYBF16 ? 2 : 4), g_bytes,
-                  &st.full[s]);
-        if (has_dh)
-            bulk_load(buf + h_bytes + g_bytes, static_cast<const uint8_t *>(a.dh) + row * a.ld_dh * (SBF16 ? 2 : 4),
-                      h_bytes, &st.full[s]);
+        const HRow h(a.h, row, a.ld_h, cols), d(a.dh, row, a.ld_dh, cols);
+        const GRow g(a.dy, row, a.ld_dy, cols);
+        mbar_arrive_expect_tx(&st.full[s], h.bytes + g.bytes + (has_dh ? d.bytes : 0u));
+        bulk_load(buf, h.src, h.bytes, &st.full[s]);
+        bulk_load(buf + g_at, g.src, g.bytes, &st.full[s]);
+        if (has_dh) bulk_load(buf + d_at, d.src, d.bytes, &st.full[s]);
     };
     if (t == 0) {
         for (int s = 0; s < a.stages; ++s) mbar_init(&st.full[s], 1);
@@ -604,14 +613,17 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_backward_ring_kernel(const __g
         const float r = a.rstd[row];
         bad = !mbar_wait(&st.full[s], parity, kErrTimeoutTransform, &st.abort);
         const uint8_t *buf = ring + s * a.stage_bytes;
+        const uint8_t *h_row = buf + HRow(a.h, row, a.ld_h, cols).shift;
+        const uint8_t *g_row = buf + g_at + GRow(a.dy, row, a.ld_dy, cols).shift;
+        const uint8_t *d_row = buf + d_at + HRow(a.dh, row, a.ld_dh, cols).shift;
         float xh[NV][8], g[NV][8], d[NV][8];
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = 8 * (t + 32 * W * j);
-            load8s<SBF16>(buf, col, col < cols, xh[j]);
-            load8s<DYBF16>(buf + h_bytes, col, col < cols, g[j]);
-            load8s<SBF16>(buf + h_bytes + g_bytes, col, has_dh && col < cols, d[j]);
+            load8<SBF16, VEC>(h_row, col, cols - col, xh[j]);
+            load8<DYBF16, VEC>(g_row, col, cols - col, g[j]);
+            load8<SBF16, VEC>(d_row, col, has_dh ? cols - col : 0, d[j]);
             if constexpr (!kHoldWeight) load_weight8(a.weight, a.weight_bf16, col, cols - col, a.vec_weight, w[j]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -629,7 +641,7 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_backward_ring_kernel(const __g
             const int col = 8 * (t + 32 * W * j);
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[j][e] = fmaf(r, g[j][e] - xh[j][e] * dot, d[j][e]);
-            put8<DXBF16, true>(a.dx, row * a.ld_dx + col, cols - col, d[j]);
+            put8<DXBF16, VEC>(a.dx, row * a.ld_dx + col, cols - col, d[j]);
         }
         if (++s == a.stages) {
             s = 0;
@@ -640,83 +652,47 @@ __global__ void __launch_bounds__(32 * W) rmsnorm_backward_ring_kernel(const __g
     if (a.dweight != nullptr) write_partial<W, NV>(a, dw);
 }
 
-template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8>
-cudaError_t launch_fwd_vec(const NormArgs &a, cudaStream_t stream) {
-    using S = RowShape<W>;
-    const unsigned grid = static_cast<unsigned>((a.rows + S::kRows - 1) / S::kRows);
-    if (a.vec)
-        rmsnorm_kernel<W, NV, SBF16, XBF16, RES, OUT8, true><<<grid, S::kThreads, 0, stream>>>(a);
-    else
-        rmsnorm_kernel<W, NV, SBF16, XBF16, RES, OUT8, false><<<grid, S::kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+// The stream's, dy's and dx's types as compile-time choices.
+template <typename F>
+cudaError_t with_bwd_types(const NormBwdArgs &a, F f) {
+    using T = std::true_type;
+    using N = std::false_type;
+    switch ((a.stream_bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.dx_bf16 ? 1 : 0)) {
+        case 0: return f(N(), N(), N());
+        case 1: return f(N(), N(), T());
+        case 2: return f(N(), T(), N());
+        case 3: return f(N(), T(), T());
+        case 4: return f(T(), N(), N());
+        case 5: return f(T(), N(), T());
+        case 6: return f(T(), T(), N());
+        default: return f(T(), T(), T());
+    }
 }
 
 template <int W, int NV>
-cudaError_t launch_fwd_shape(const NormArgs &a, cudaStream_t stream) {
-    const bool out8 = a.elems8 != nullptr;
-    if (a.residual == nullptr) {     // the stream is x itself
-        if (a.x_bf16)
-            return out8 ? launch_fwd_vec<W, NV, true, true, false, true>(a, stream)
-                        : launch_fwd_vec<W, NV, true, true, false, false>(a, stream);
-        return out8 ? launch_fwd_vec<W, NV, false, false, false, true>(a, stream)
-                    : launch_fwd_vec<W, NV, false, false, false, false>(a, stream);
-    }
-    switch ((a.stream_bf16 ? 4 : 0) | (a.x_bf16 ? 2 : 0) | (out8 ? 1 : 0)) {
-        case 0: return launch_fwd_vec<W, NV, false, false, true, false>(a, stream);
-        case 1: return launch_fwd_vec<W, NV, false, false, true, true>(a, stream);
-        case 2: return launch_fwd_vec<W, NV, false, true, true, false>(a, stream);
-        case 3: return launch_fwd_vec<W, NV, false, true, true, true>(a, stream);
-        case 4: return launch_fwd_vec<W, NV, true, false, true, false>(a, stream);
-        case 5: return launch_fwd_vec<W, NV, true, false, true, true>(a, stream);
-        case 6: return launch_fwd_vec<W, NV, true, true, true, false>(a, stream);
-        default: return launch_fwd_vec<W, NV, true, true, true, true>(a, stream);
-    }
-}
-
-template <int W, int NV, bool SBF16, bool DYBF16, bool DXBF16>
-cudaError_t launch_bwd_vec(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
-    using S = RowShape<W>;
-    const unsigned grid = static_cast<unsigned>(blocks);
-    // aligned rows of up to 1024 elements have their own kernel, and those of
-    // 1025 to 8192 always fit the ring
-    if constexpr (W > 8) {
-        if (a.vec) {
-            rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, true><<<grid, S::kThreads, 0, stream>>>(a);
-            return cudaGetLastError();
-        }
-    }
-    rmsnorm_backward_kernel<W, NV, SBF16, DYBF16, DXBF16, false><<<grid, S::kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_bwd_rows(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
+    const unsigned n = static_cast<unsigned>(blocks);
+    return with_bwd_types(a, [&](auto s, auto g, auto d) {
+        constexpr bool S = decltype(s)::value, G = decltype(g)::value, D = decltype(d)::value;
+        if (a.vec)
+            rmsnorm_backward_kernel<W, NV, S, G, D, true><<<n, 32 * W, 0, stream>>>(a);
+        else
+            rmsnorm_backward_kernel<W, NV, S, G, D, false><<<n, 32 * W, 0, stream>>>(a);
+        return cudaGetLastError();
+    });
 }
 
 template <int NV, int U>
 cudaError_t launch_bwd_short(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
     const unsigned n = static_cast<unsigned>(blocks);
-    switch ((a.stream_bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.dx_bf16 ? 1 : 0)) {
-        case 0: rmsnorm_backward_short_kernel<NV, U, false, false, false><<<n, 128, 0, stream>>>(a); break;
-        case 1: rmsnorm_backward_short_kernel<NV, U, false, false, true><<<n, 128, 0, stream>>>(a); break;
-        case 2: rmsnorm_backward_short_kernel<NV, U, false, true, false><<<n, 128, 0, stream>>>(a); break;
-        case 3: rmsnorm_backward_short_kernel<NV, U, false, true, true><<<n, 128, 0, stream>>>(a); break;
-        case 4: rmsnorm_backward_short_kernel<NV, U, true, false, false><<<n, 128, 0, stream>>>(a); break;
-        case 5: rmsnorm_backward_short_kernel<NV, U, true, false, true><<<n, 128, 0, stream>>>(a); break;
-        case 6: rmsnorm_backward_short_kernel<NV, U, true, true, false><<<n, 128, 0, stream>>>(a); break;
-        default: rmsnorm_backward_short_kernel<NV, U, true, true, true><<<n, 128, 0, stream>>>(a); break;
-    }
-    return cudaGetLastError();
-}
-
-template <int W, int NV>
-cudaError_t launch_bwd_shape(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
-    switch ((a.stream_bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.dx_bf16 ? 1 : 0)) {
-        case 0: return launch_bwd_vec<W, NV, false, false, false>(a, blocks, stream);
-        case 1: return launch_bwd_vec<W, NV, false, false, true>(a, blocks, stream);
-        case 2: return launch_bwd_vec<W, NV, false, true, false>(a, blocks, stream);
-        case 3: return launch_bwd_vec<W, NV, false, true, true>(a, blocks, stream);
-        case 4: return launch_bwd_vec<W, NV, true, false, false>(a, blocks, stream);
-        case 5: return launch_bwd_vec<W, NV, true, false, true>(a, blocks, stream);
-        case 6: return launch_bwd_vec<W, NV, true, true, false>(a, blocks, stream);
-        default: return launch_bwd_vec<W, NV, true, true, true>(a, blocks, stream);
-    }
+    return with_bwd_types(a, [&](auto s, auto g, auto d) {
+        constexpr bool S = decltype(s)::value, G = decltype(g)::value, D = decltype(d)::value;
+        if (a.vec)
+            rmsnorm_backward_short_kernel<NV, U, S, G, D, true><<<n, 128, 0, stream>>>(a);
+        else
+            rmsnorm_backward_short_kernel<NV, U, S, G, D, false><<<n, 128, 0, stream>>>(a);
+        return cudaGetLastError();
+    });
 }
 
 // Width of the rings: warps per row with two vectors per thread.
@@ -750,11 +726,11 @@ int64_t bwd_blocks(int64_t rows, int64_t cols) {
     return need < most ? need : most;
 }
 
-template <int W, bool SBF16, bool XBF16, bool RES, bool OUT8>
-cudaError_t launch_fwd_ring(const NormArgs &a, cudaStream_t stream) {
+template <int W, bool SBF16, bool XBF16, bool RES, bool OUT8, bool VEC>
+cudaError_t launch_fwd_ring_kernel(const NormArgs &a, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     const int smem = a.stages * static_cast<int>(a.stage_bytes);
-    auto *kernel = rmsnorm_ring_kernel<W, 2, SBF16, XBF16, RES, OUT8>;
+    auto *kernel = rmsnorm_ring_kernel<W, 2, SBF16, XBF16, RES, OUT8, VEC>;
     const cudaError_t e = allow_smem(kernel, kRingSmem, done);
     if (e != cudaSuccess) return e;
     const int64_t most = int64_t(148) * fwd_blocks_per_sm(a.kpad);
@@ -762,33 +738,56 @@ cudaError_t launch_fwd_ring(const NormArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <int W>
-cudaError_t launch_fwd_ring_types(const NormArgs &a, cudaStream_t stream) {
+// x's and the stream's types, the residual and the output as compile-time choices.
+template <typename F>
+cudaError_t with_fwd_types(const NormArgs &a, F f) {
+    using T = std::true_type;
+    using N = std::false_type;
     const bool out8 = a.elems8 != nullptr;
-    if (a.residual == nullptr) {
-        if (a.x_bf16)
-            return out8 ? launch_fwd_ring<W, true, true, false, true>(a, stream)
-                        : launch_fwd_ring<W, true, true, false, false>(a, stream);
-        return out8 ? launch_fwd_ring<W, false, false, false, true>(a, stream)
-                    : launch_fwd_ring<W, false, false, false, false>(a, stream);
+    if (a.residual == nullptr) {     // the stream is x itself
+        if (a.x_bf16) return out8 ? f(T(), T(), N(), T()) : f(T(), T(), N(), N());
+        return out8 ? f(N(), N(), N(), T()) : f(N(), N(), N(), N());
     }
     switch ((a.stream_bf16 ? 4 : 0) | (a.x_bf16 ? 2 : 0) | (out8 ? 1 : 0)) {
-        case 0: return launch_fwd_ring<W, false, false, true, false>(a, stream);
-        case 1: return launch_fwd_ring<W, false, false, true, true>(a, stream);
-        case 2: return launch_fwd_ring<W, false, true, true, false>(a, stream);
-        case 3: return launch_fwd_ring<W, false, true, true, true>(a, stream);
-        case 4: return launch_fwd_ring<W, true, false, true, false>(a, stream);
-        case 5: return launch_fwd_ring<W, true, false, true, true>(a, stream);
-        case 6: return launch_fwd_ring<W, true, true, true, false>(a, stream);
-        default: return launch_fwd_ring<W, true, true, true, true>(a, stream);
+        case 0: return f(N(), N(), T(), N());
+        case 1: return f(N(), N(), T(), T());
+        case 2: return f(N(), T(), T(), N());
+        case 3: return f(N(), T(), T(), T());
+        case 4: return f(T(), N(), T(), N());
+        case 5: return f(T(), N(), T(), T());
+        case 6: return f(T(), T(), T(), N());
+        default: return f(T(), T(), T(), T());
     }
 }
 
-template <int W, bool SBF16, bool DYBF16, bool DXBF16>
-cudaError_t launch_bwd_ring(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
+template <int W>
+cudaError_t launch_fwd_ring(const NormArgs &a, cudaStream_t stream) {
+    return with_fwd_types(a, [&](auto s, auto x, auto r, auto o) {
+        constexpr bool S = decltype(s)::value, X = decltype(x)::value, R = decltype(r)::value, O = decltype(o)::value;
+        return a.vec ? launch_fwd_ring_kernel<W, S, X, R, O, true>(a, stream)
+                     : launch_fwd_ring_kernel<W, S, X, R, O, false>(a, stream);
+    });
+}
+
+template <int W, int NV>
+cudaError_t launch_fwd_rows(const NormArgs &a, cudaStream_t stream) {
+    using S = RowShape<W>;
+    const unsigned grid = static_cast<unsigned>((a.rows + S::kRows - 1) / S::kRows);
+    return with_fwd_types(a, [&](auto s, auto x, auto r, auto o) {
+        constexpr bool SB = decltype(s)::value, X = decltype(x)::value, R = decltype(r)::value, O = decltype(o)::value;
+        if (a.vec)
+            rmsnorm_kernel<W, NV, SB, X, R, O, true><<<grid, S::kThreads, 0, stream>>>(a);
+        else
+            rmsnorm_kernel<W, NV, SB, X, R, O, false><<<grid, S::kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    });
+}
+
+template <int W, bool SBF16, bool DYBF16, bool DXBF16, bool VEC>
+cudaError_t launch_bwd_ring_kernel(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     const int smem = a.stages * static_cast<int>(a.stage_bytes);
-    auto *kernel = rmsnorm_backward_ring_kernel<W, 2, SBF16, DYBF16, DXBF16>;
+    auto *kernel = rmsnorm_backward_ring_kernel<W, 2, SBF16, DYBF16, DXBF16, VEC>;
     const cudaError_t e = allow_smem(kernel, kRingSmem, done);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(blocks), 32 * W, smem, stream>>>(a);
@@ -796,43 +795,39 @@ cudaError_t launch_bwd_ring(const NormBwdArgs &a, int64_t blocks, cudaStream_t s
 }
 
 template <int W>
-cudaError_t launch_bwd_ring_types(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
-    switch ((a.stream_bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.dx_bf16 ? 1 : 0)) {
-        case 0: return launch_bwd_ring<W, false, false, false>(a, blocks, stream);
-        case 1: return launch_bwd_ring<W, false, false, true>(a, blocks, stream);
-        case 2: return launch_bwd_ring<W, false, true, false>(a, blocks, stream);
-        case 3: return launch_bwd_ring<W, false, true, true>(a, blocks, stream);
-        case 4: return launch_bwd_ring<W, true, false, false>(a, blocks, stream);
-        case 5: return launch_bwd_ring<W, true, false, true>(a, blocks, stream);
-        case 6: return launch_bwd_ring<W, true, true, false>(a, blocks, stream);
-        default: return launch_bwd_ring<W, true, true, true>(a, blocks, stream);
-    }
+cudaError_t launch_bwd_ring(const NormBwdArgs &a, int64_t blocks, cudaStream_t stream) {
+    return with_bwd_types(a, [&](auto s, auto g, auto d) {
+        constexpr bool S = decltype(s)::value, G = decltype(g)::value, D = decltype(d)::value;
+        return a.vec ? launch_bwd_ring_kernel<W, S, G, D, true>(a, blocks, stream)
+                     : launch_bwd_ring_kernel<W, S, G, D, false>(a, blocks, stream);
+    });
 }
+
+// Shared memory of a row of `cols` elements of `size` bytes in a stage.
+int64_t staged_room(int64_t cols, int64_t size, bool vec) { return (cols * size + 15) / 16 * 16 + (vec ? 0 : 16); }
 
 }  // namespace
 
-// Rows of more than 1024 elements that bulk copies can fetch (vec: 16-byte
-// aligned rows) go through the ring once a block gets more than one of them;
-// short rows have a warp each, and few, odd or very long rows a block each.
+// Rows of more than 1024 elements go through the ring once an SM gets more than
+// one of them; short rows have a warp each, and few or very long rows a block
+// each.
 cudaError_t launch_rmsnorm(const NormArgs &args, cudaStream_t stream) {
     NormArgs a = args;
     const int64_t width = a.kpad;
-    if (a.vec && width > 1024 && width <= 16384 && a.rows > int64_t(148) * fwd_blocks_per_sm(width)) {
-        const int64_t bytes = a.cols * ((a.x_bf16 ? 2 : 4) + (a.residual == nullptr ? 0 : a.stream_bf16 ? 2 : 4));
+    if (width > 1024 && width <= 16384 && a.rows > 148) {
+        int64_t bytes = staged_room(a.cols, a.x_bf16 ? 2 : 4, a.vec);
+        if (a.residual != nullptr) bytes += staged_room(a.cols, a.stream_bf16 ? 2 : 4, a.vec);
         a.stages = ring_stages(bytes, fwd_blocks_per_sm(width));
         a.stage_bytes = (bytes + 127) / 128 * 128;
         if (a.stages >= 2)
-            return with_ring_shape(width, [&](auto w) { return launch_fwd_ring_types<decltype(w)::value>(a, stream); });
+            return with_ring_shape(width, [&](auto w) { return launch_fwd_ring<decltype(w)::value>(a, stream); });
     }
-    if (width <= 256) return launch_fwd_shape<1, 1>(a, stream);
-    if (width <= 1024) return launch_fwd_shape<1, 4>(a, stream);
-    // a row or less for each SM: one vector per thread (one token of 8192: 8.0 -> 4.3 us)
-    if (a.rows <= 148 && width <= 8192)
-        return width <= 2048 ? launch_fwd_shape<8, 1>(a, stream) : launch_fwd_shape<32, 1>(a, stream);
-    if (width <= 4096) return launch_fwd_shape<4, 4>(a, stream);
-    if (width <= 8192) return launch_fwd_shape<8, 4>(a, stream);
-    if (width <= 16384) return launch_fwd_shape<16, 4>(a, stream);
-    return launch_fwd_shape<32, 4>(a, stream);
+    if (width <= 256) return launch_fwd_rows<1, 1>(a, stream);
+    if (width <= 1024) return launch_fwd_rows<1, 4>(a, stream);
+    // one vector per thread (one token of 8192: 8.0 us with four, 4.3 with one)
+    if (width <= 2048) return launch_fwd_rows<8, 1>(a, stream);
+    if (width <= 8192) return launch_fwd_rows<32, 1>(a, stream);
+    return launch_fwd_rows<32, 4>(a, stream);
 }
 
 int64_t rmsnorm_backward_slots(int64_t rows, int64_t cols) { return rows <= 0 ? 0 : bwd_blocks(rows, cols); }
@@ -842,29 +837,23 @@ cudaError_t launch_rmsnorm_backward(const NormBwdArgs &args, cudaStream_t stream
     const int64_t blocks = bwd_blocks(a.rows, a.cols);
     cudaError_t e = cudaErrorInvalidValue;
     bool ring = false;
-    if (a.vec && a.cols > 1024 && a.cols <= 16384) {
-        const int64_t st = a.stream_bf16 ? 2 : 4;
-        const int64_t bytes = a.cols * ((a.dh == nullptr ? st : 2 * st) + (a.dy_bf16 ? 2 : 4));
+    if (a.cols > 1024 && a.cols <= 16384) {
+        const int64_t st = staged_room(a.cols, a.stream_bf16 ? 2 : 4, a.vec);
+        const int64_t bytes = (a.dh == nullptr ? st : 2 * st) + staged_room(a.cols, a.dy_bf16 ? 2 : 4, a.vec);
         a.stages = ring_stages(bytes, bwd_blocks_per_sm(a.cols));
         a.stage_bytes = (bytes + 127) / 128 * 128;
         ring = a.stages >= 2;
     }
     if (ring)
-        e = with_ring_shape(a.cols, [&](auto w) { return launch_bwd_ring_types<decltype(w)::value>(a, blocks, stream); });
-    else if (a.cols <= 1024 && a.vec)
-        e = a.cols <= 256   ? launch_bwd_short<1, 4>(a, blocks, stream)
-            : a.cols <= 512 ? launch_bwd_short<2, 2>(a, blocks, stream)
-                            : launch_bwd_short<4, 1>(a, blocks, stream);
+        e = with_ring_shape(a.cols, [&](auto w) { return launch_bwd_ring<decltype(w)::value>(a, blocks, stream); });
+    else if (a.cols <= 256)
+        e = launch_bwd_short<1, 4>(a, blocks, stream);
+    else if (a.cols <= 512)
+        e = launch_bwd_short<2, 2>(a, blocks, stream);
     else if (a.cols <= 1024)
-        e = launch_bwd_shape<1, 4>(a, blocks, stream);
-    else if (a.cols <= 4096)
-        e = launch_bwd_shape<4, 4>(a, blocks, stream);
-    else if (a.cols <= 8192)
-        e = launch_bwd_shape<8, 4>(a, blocks, stream);
-    else if (a.cols <= 16384)
-        e = launch_bwd_shape<16, 4>(a, blocks, stream);
+        e = launch_bwd_short<4, 1>(a, blocks, stream);
     else
-        e = launch_bwd_shape<32, 4>(a, blocks, stream);
+        e = launch_bwd_rows<32, 4>(a, blocks, stream);
     if (e != cudaSuccess || a.dweight == nullptr) return e;
     return launch_column_sums(a.partial, blocks, a.cols, a.dweight, stream);
 }

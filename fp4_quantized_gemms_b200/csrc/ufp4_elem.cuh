@@ -83,8 +83,133 @@ __device__ __forceinline__ void store_quad(void *p, int64_t i, bool bf16, bool v
         if (e < valid) store_elem(p, i + e, bf16, e4[e]);
 }
 
-// Eight elements of a row as loaded, bf16 or fp32 (16-byte aligned, read once:
-// evict first).
+// ---------------------------------------------------------------------------
+// Eight consecutive elements at any element alignment (odd widths and pitches,
+// views that start anywhere), as fast as the alignment allows: whole 16-byte
+// granules are moved, and a funnel shift lines them up.
+
+// Moves words [shift, ..) of w to its front; shift in 0 .. 3, the same for the
+// warp's lanes.
+template <int N>
+__device__ __forceinline__ void drop_words(uint32_t (&w)[N], int shift) {
+    if (shift & 2) {
+#pragma unroll
+        for (int k = 0; k + 2 < N; ++k) w[k] = w[k + 2];
+    }
+    if (shift & 1) {
+#pragma unroll
+        for (int k = 0; k + 1 < N; ++k) w[k] = w[k + 1];
+    }
+}
+
+// Elements p[i .. i + 7] (global or shared memory) as stored, those at or
+// beyond `valid` as 0.  A granule is read only when it holds a valid element
+// (so never outside that element's page); what else it holds is not used.
+template <bool BF16>
+__device__ __forceinline__ void load8_raw(const void *p, int64_t i, int valid, uint32_t (&o)[BF16 ? 4 : 8]) {
+    constexpr int kSize = BF16 ? 2 : 4, kGranules = BF16 ? 2 : 3;
+    const uintptr_t addr = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(i * kSize);
+    const int s = static_cast<int>(addr & 15u);
+    const uint4 *g = reinterpret_cast<const uint4 *>(addr - static_cast<uintptr_t>(s));
+    const int bytes = (valid < 8 ? valid : 8) * kSize + s;
+    uint32_t w[4 * kGranules];
+#pragma unroll
+    for (int k = 0; k < kGranules; ++k) {
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (valid > 0 && 16 * k < bytes) q = g[k];
+        w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
+    }
+    drop_words(w, s >> 2);
+    if constexpr (BF16) {
+        const int bits = (s & 2) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(w[k], w[k + 1], bits);
+        if (valid < 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = 2 * k >= valid ? 0u : 2 * k + 1 >= valid ? o[k] & 0xFFFFu : o[k];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = k < valid ? w[k] : 0u;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8_any(const void *p, int64_t i, int valid, float (&v)[8]) {
+    uint32_t o[BF16 ? 4 : 8];
+    load8_raw<BF16>(p, i, valid, o);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = BF16 ? ((k & 1) ? bf16_hi(o[k / 2]) : bf16_lo(o[k / 2])) : __uint_as_float(o[BF16 ? 0 : k]);
+}
+
+// Stores eight elements per lane, lane l's right behind lane l - 1's (p[i]
+// differs by 8 from lane to lane); `rest`: elements of the row from this
+// lane's first on (any number; none are stored beyond it).  All 32 lanes take
+// part.  A granule that two lanes share is written by the second, from the
+// first one's last words; what the warp does not fill whole is written
+// element by element.
+template <bool BF16>
+__device__ __forceinline__ void store8_any(void *p, int64_t i, int rest, const float (&v)[8]) {
+    constexpr int kSize = BF16 ? 2 : 4, kWords = BF16 ? 4 : 8;
+    const uintptr_t addr = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(i * kSize);
+    const int s = static_cast<int>(addr & 15u);           // the same in all lanes
+    const int lane = threadIdx.x & 31;
+    uint32_t w[4 + kWords];                                // the last 16 bytes of the lane before, then this one's
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+        w[4 + k] = BF16 ? pack_bf16(v[(2 * k) % 8], v[(2 * k + 1) % 8]) : __float_as_uint(v[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __shfl_up_sync(0xFFFFFFFFu, w[kWords + k], 1);
+    // bytes [16 - s, ..) of the 16 + 4 kWords: the granules from addr - s on
+    const int head = s == 0 ? 0 : (16 - s) / kSize;        // this lane's elements in the shared granule
+    const int have = rest < 8 ? rest : 8;
+    const bool shared = s != 0 && lane > 0 && rest >= head;
+    const bool next = s != 0 && lane < 31 && rest - 8 >= head;   // the next lane writes this one's end
+    uint32_t o[4 + kWords];
+#pragma unroll
+    for (int k = 0; k < 4 + kWords; ++k) o[k] = w[k];
+    drop_words(o, s == 0 ? 0 : (16 - s) >> 2);
+    if constexpr (BF16) {
+        const int bits = (s & 2) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = __funnelshift_r(o[k], o[k + 1], bits);
+    }
+    uint4 *g = reinterpret_cast<uint4 *>(addr - static_cast<uintptr_t>(s));
+    int done_to = 0, done_from = 0;                        // elements [done_from, done_to) are in granules
+    if (s == 0) {
+        constexpr int kOwn = BF16 ? 1 : 2;
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q) {
+            if (have >= (q + 1) * 16 / kSize) {
+                g[q] = make_uint4(w[4 + 4 * q], w[5 + 4 * q], w[6 + 4 * q], w[7 + 4 * q]);
+                done_to = (q + 1) * 16 / kSize;
+            }
+        }
+    } else {
+        done_from = head;
+        if (shared) {
+            g[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            done_from = 0;
+        }
+        done_to = head;
+        if constexpr (!BF16) {                             // one granule is the lane's own
+            if (have >= head + 4) {
+                g[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                done_to = head + 4;
+            }
+        }
+        if (next) done_to = 8;
+    }
+    if (done_from > 0 || done_to < have) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < have && (k < done_from || k >= done_to)) store_elem(p, i + k, BF16, v[k]);
+    }
+}
+
+// Eight elements of a row as loaded, bf16 or fp32 (load: 16-byte aligned, read
+// once, evict first).
 template <bool BF16>
 struct Raw8 {
     uint4 w[BF16 ? 1 : 2];
@@ -93,6 +218,13 @@ struct Raw8 {
                               : reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
         w[0] = __ldcs(q);
         if constexpr (!BF16) w[1] = __ldcs(q + 1);
+    }
+    // any alignment; elements at or beyond `valid` as 0
+    __device__ __forceinline__ void load_any(const void *p, int64_t i, int valid) {
+        uint32_t o[BF16 ? 4 : 8];
+        load8_raw<BF16>(p, i, valid, o);
+        w[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        if constexpr (!BF16) w[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
     __device__ __forceinline__ void zero() {
         w[0] = make_uint4(0u, 0u, 0u, 0u);
@@ -152,6 +284,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2A = 2.0f * 0.79788456080286536f;          // 2 sqrt(2 / pi)
 constexpr float kGelu2B = kGelu2A * 0.044715f;
 
+// erf by Abramowitz and Stegun 7.1.26: within 1.5e-7, in 12 operations.
+__device__ __forceinline__ float erf_approx(float x) {
+    const float a = fabsf(x);
+    const float t = rcp_approx(fmaf(0.3275911f, a, 1.0f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float y = fmaf(-p * t, ex2_approx(-kLog2e * a * a), 1.0f);
+    return copysignf(y, x);
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
     switch (act) {
         case UFP4_ACT_RELU: return z < 0.0f ? 0.0f : z;          // NaN stays NaN
@@ -159,7 +303,7 @@ __device__ __forceinline__ float act_value(float z, int act) {
             const float p = fmaf(-kGelu2B * kLog2e, z * z, -kGelu2A * kLog2e);
             return z * rcp_approx(1.0f + ex2_approx(z * p));
         }
-        case UFP4_ACT_GELU_ERF: return 0.5f * z * (1.0f + erff(0.70710678118654752f * z));
+        case UFP4_ACT_GELU_ERF: return 0.5f * z * (1.0f + erf_approx(0.70710678118654752f * z));
         case UFP4_ACT_SILU: return z * rcp_approx(1.0f + ex2_approx(-kLog2e * z));
         default: return z;
     }
@@ -205,7 +349,7 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         auto one = [](float v) {
             const float c = clamp_nan(v, 9.0f);
             return fmaf(c * 0.39894228040143268f, ex2_approx(-0.5f * kLog2e * c * c),
-                        0.5f * (1.0f + erff(0.70710678118654752f * c)));
+                        0.5f * (1.0f + erf_approx(0.70710678118654752f * c)));
         };
         return make_float2(one(z.x), one(z.y));
     } else {

@@ -186,6 +186,10 @@ constexpr int pair_stage_k(int grid_kind, bool atoms) { return (grid_kind == 1 &
 cudaError_t launch_gemm(const GemmArgs &args, int mode, int grid_kind, int num_sms,
                         cudaStream_t stream);
 
+// The same kernels with args.epi (gemm_epilogue.cu, gemm_epilogue_mx.cu).
+cudaError_t launch_gemm_epilogue(const GemmArgs &args, int mode, int grid_kind, int num_sms, cudaStream_t stream);
+cudaError_t launch_gemm_epilogue_mx(const GemmArgs &args, int num_sms, cudaStream_t stream);
+
 // out = act(bias) + residual: the epilogue of a product without a reduction
 // dimension (k = 0).
 cudaError_t launch_epilogue_only(const EpiArgs &e, int64_t m, int64_t n, int num_sms, cudaStream_t stream);

@@ -107,7 +107,7 @@ def test_parts_and_types(act, out, bias_t, res_t, pre_t):
 
 
 @pytest.mark.parametrize("fmt", ["e2m1_two", "mx", "e1m2_fp32", "e1m2_nocorr"])
-@pytest.mark.parametrize("pad,offset", [(1, 0), (3, 1), (4, 0), (8, 4)])
+@pytest.mark.parametrize("pad,offset", [(1, 0), (3, 1), (4, 0), (8, 4), (5, 0), (13, 8)])
 def test_pitch_and_alignment(fmt, pad, offset):
     """Row pitches and start addresses that forbid vector accesses, odd N; the
     padding between rows stays as it was."""
@@ -226,7 +226,7 @@ def _check_bwd(dpre, dbias, dout, pre, act, terms=1.0):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("gt,zt,dt", [(BF16, BF16, BF16), (FP32, BF16, BF16), (FP32, FP32, FP32), (BF16, FP32, FP32)])
-@pytest.mark.parametrize("m,n", [(1, 8), (77, 264), (1030, 1408), (40, 131)])
+@pytest.mark.parametrize("m,n", [(1, 8), (77, 264), (1030, 1408), (40, 131), (1100, 1021)])
 def test_backward(act, gt, zt, dt, m, n):
     dout, pre = rand(1, m, n, std=0.01, dtype=gt), rand(2, m, n, std=3.0, dtype=zt)
     dpre, dbias = ufp4.epilogue_backward(dout, pre, ACTS[act], dpre=torch.empty(m, n, dtype=dt, device="cuda"))
@@ -238,9 +238,11 @@ def test_backward(act, gt, zt, dt, m, n):
 def test_backward_pitch(pad, offset):
     m, n = 100, 264
     dout, pre = strided(rand(1, m, n), pad, offset), strided(rand(2, m, n), pad + 8, offset)
-    dpre, dbias = ufp4.epilogue_backward(dout, pre, ufp4.ACT_SILU)
+    buf = torch.full((m * (n + pad) + offset,), 7.0, dtype=BF16, device="cuda")
+    dpre, dbias = ufp4.epilogue_backward(dout, pre, ufp4.ACT_SILU, dpre=buf[offset:].view(m, n + pad)[:, :n])
     _ok()
     _check_bwd(dpre, dbias, dout, pre, "silu")
+    assert bool((buf[offset:].view(m, n + pad)[:, n:] == 7.0).all()) and bool((buf[:offset] == 7.0).all())
 
 
 def test_backward_in_place_without_activation_and_empty():

@@ -21,6 +21,16 @@ def _ok():
     assert ufp4.check_device_status() == ufp4.OK
 
 
+def _around(v):
+    """What the allocation of a strided matrix holds beside its rows."""
+    whole = torch.empty(0, dtype=v.dtype, device=v.device).set_(v.untyped_storage())
+    mine = torch.zeros(whole.numel(), dtype=torch.bool, device=v.device)
+    r, c = v.shape
+    mine[(v.storage_offset() + torch.arange(r, device=v.device)[:, None] * v.stride(0) +
+          torch.arange(c, device=v.device)).reshape(-1)] = True
+    return whole[~mine]
+
+
 def _expect(x, res, w, eps=EPS):
     h = x.double() if res is None else (x.double() + res.double()).to(res.dtype).double()
     r = 1 / torch.sqrt((h * h).mean(1) + eps)
@@ -61,7 +71,7 @@ COLS = [1, 7, 31, 64, 100, 256, 257, 520, 1000, 1024, 1032, 1408, 2048, 4096, 41
 
 
 @pytest.mark.parametrize("cols", COLS)
-@pytest.mark.parametrize("rows", [1, 5, 133])
+@pytest.mark.parametrize("rows", [1, 5, 133, 700])
 @pytest.mark.parametrize("eight", [False, True])
 def test_widths(rows, cols, eight):
     x, res, w = rand(1, rows, cols), rand(2, rows, cols, std=2.0), rand(3, cols)
@@ -80,7 +90,8 @@ def test_widths(rows, cols, eight):
 
 @pytest.mark.parametrize("xt,st,wt", [(BF16, None, FP32), (FP32, None, BF16), (FP32, FP32, FP32), (BF16, FP32, BF16),
                                       (FP32, BF16, BF16)])
-@pytest.mark.parametrize("rows,cols", [(9, 96), (200, 1000), (40, 2056), (12, 8192), (6, 30000)])
+@pytest.mark.parametrize("rows,cols", [(9, 96), (200, 1000), (300, 1027), (40, 2056), (1300, 2055), (12, 8192),
+                                       (200, 12345), (6, 30000)])
 @pytest.mark.parametrize("eight", [False, True])
 def test_types(xt, st, wt, rows, cols, eight):
     x, w = rand(1, rows, cols, dtype=xt), rand(3, cols, dtype=wt)
@@ -103,15 +114,16 @@ def test_types(xt, st, wt, rows, cols, eight):
 
 
 @pytest.mark.parametrize("pad,offset", [(1, 0), (8, 0), (8, 1), (3, 5)])
-@pytest.mark.parametrize("cols", [264, 1410])
-def test_pitch_and_alignment(cols, pad, offset):
-    rows = 70
+@pytest.mark.parametrize("rows,cols", [(70, 264), (70, 1410), (400, 1410), (300, 3001)])
+def test_pitch_and_alignment(rows, cols, pad, offset):
     x, res, w = rand(1, rows, cols), rand(2, rows, cols), rand(3, cols + 1)[1:]
     y = strided(torch.full((rows, cols), 7.0, dtype=BF16, device="cuda"), pad, offset)
     y0, _, h0, r0 = ufp4.rmsnorm(x, w, residual=res, eps=EPS)
     hv = strided(res, pad, offset)
+    around = [(v, _around(v).clone()) for v in (y, hv)]
     _, _, h, r = ufp4.rmsnorm(strided(x, pad, offset), w, residual=hv, h=hv, eps=EPS, y=y)
     _ok()
+    assert all(torch.equal(_around(v), keep) for v, keep in around)      # nothing beside the rows was written
     h64, _, y64 = _expect(x, res, w)
     assert h is hv and torch.equal(h, h0) and torch.equal(h.double(), h64)
     assert bool(((y.double() - y64).abs() <= (half_step(BF16) * 1.001 + ARITH) * y64.abs()).all())
@@ -231,7 +243,8 @@ def test_backward_widths(rows, cols):
 
 @pytest.mark.parametrize("gt,st,dt,wt", [(FP32, BF16, BF16, FP32), (BF16, FP32, FP32, BF16), (FP32, FP32, BF16, FP32),
                                          (BF16, BF16, FP32, BF16), (BF16, FP32, BF16, BF16), (FP32, FP32, FP32, FP32)])
-@pytest.mark.parametrize("rows,cols", [(9, 96), (200, 1000), (40, 2056), (350, 8192), (6, 30000)])
+@pytest.mark.parametrize("rows,cols", [(9, 96), (200, 1000), (300, 509), (40, 2056), (700, 2055), (350, 8192),
+                                       (150, 12345), (6, 30000)])
 @pytest.mark.parametrize("with_dh", [False, True])
 def test_backward_types(gt, st, dt, wt, rows, cols, with_dh):
     dy, h, w = rand(1, rows, cols, dtype=gt), rand(2, rows, cols, dtype=st), rand(3, cols, dtype=wt)
@@ -243,14 +256,16 @@ def test_backward_types(gt, st, dt, wt, rows, cols, with_dh):
 
 
 @pytest.mark.parametrize("pad,offset", [(1, 0), (8, 0), (8, 1)])
-def test_backward_pitch_in_place_and_empty(pad, offset):
-    rows, cols = 90, 520
+@pytest.mark.parametrize("rows,cols", [(90, 520), (700, 1411)])
+def test_backward_pitch_in_place_and_empty(rows, cols, pad, offset):
     dy, h, w, dh = rand(1, rows, cols), rand(2, rows, cols), rand(3, cols), rand(4, rows, cols)
     rstd = torch.rsqrt(h.double().square().mean(1) + EPS).float()
     want, wdw = ufp4.rmsnorm_backward(dy, h, w, rstd, dh=dh)
     dhv = strided(dh, pad, offset)
+    keep = _around(dhv).clone()
     dx, dw = ufp4.rmsnorm_backward(strided(dy, pad, offset), strided(h, pad, offset), w, rstd, dh=dhv, dx=dhv)
     _ok()
+    assert torch.equal(_around(dhv), keep)
     assert dx is dhv
     _check_bwd(dx, dw, dy, h, w, rstd, dh)
     dx, dw = ufp4.rmsnorm_backward(dy, h, w, rstd, dh=dh, want_dweight=False)
