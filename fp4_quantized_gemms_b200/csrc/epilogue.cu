@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(kBwdThreads, 3) epilogue_backward_kernel(const
     if (a.dbias != nullptr) store_partial(a, sums, col0);
 }
 
-// Any width, row pitch and alignment (16384 x 8191: 666 us with one element per
-// access).
-template <int ACT>
+// Any width, row pitch and alignment: the same by whole granules (load8_raw,
+// store8_any).
+template <int ACT, bool DOUT_BF16, bool PRE_BF16>
 __global__ void __launch_bounds__(kBwdThreads, 2) epilogue_backward_any_kernel(const __grid_constant__ EpiBwdArgs a) {
     let_next_kernel_launch();
-    constexpr int U = 2;
+    constexpr int U = kBwdUnroll<DOUT_BF16, PRE_BF16>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kBwdCols;
     const int64_t col = col0 + 8 * lane;
@@ -127,40 +127,37 @@ __global__ void __launch_bounds__(kBwdThreads, 2) epilogue_backward_any_kernel(c
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
     for (int64_t r0 = r_first; r0 < r_end; r0 += kBwdWarps * U) {     // whole warps
-        float d[U][8], z[U][8];
+        Raw8<DOUT_BF16> g[U];
+        Raw8<PRE_BF16> z[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + kBwdWarps * u;
             const int valid = r < r_end ? rest : 0;
-            if (a.dout_bf16)
-                load8_any<true>(a.dout, r * a.ld_dout + col, valid, d[u]);
-            else
-                load8_any<false>(a.dout, r * a.ld_dout + col, valid, d[u]);
-            if constexpr (ACT != UFP4_ACT_NONE) {
-                if (a.pre_bf16)
-                    load8_any<true>(a.pre, r * a.ld_pre + col, valid, z[u]);
-                else
-                    load8_any<false>(a.pre, r * a.ld_pre + col, valid, z[u]);
-            }
+            g[u].load_any(a.dout, r * a.ld_dout + col, valid);
+            if constexpr (ACT != UFP4_ACT_NONE) z[u].load_any(a.pre, r * a.ld_pre + col, valid);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = r0 + kBwdWarps * u;
+            float d[8];
+            g[u].get(d);
             if constexpr (ACT != UFP4_ACT_NONE) {
+                float2 zv[4];
+                z[u].get2(zv);
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float2 q = mul2(make_float2(d[u][j], d[u][j + 1]), act_slope2<ACT>(make_float2(z[u][j], z[u][j + 1])));
-                    d[u][j] = q.x;
-                    d[u][j + 1] = q.y;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 q = mul2(make_float2(d[2 * j], d[2 * j + 1]), act_slope2<ACT>(zv[j]));
+                    d[2 * j] = q.x;
+                    d[2 * j + 1] = q.y;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += d[u][j];
+            for (int j = 0; j < 8; ++j) sum[j] += d[j];
             if (a.dpre != nullptr && r < r_end) {
                 if (a.dpre_bf16)
-                    store8_any<true>(a.dpre, r * a.ld_dpre + col, rest, d[u]);
+                    store8_any<true>(a.dpre, r * a.ld_dpre + col, rest, d);
                 else
-                    store8_any<false>(a.dpre, r * a.ld_dpre + col, rest, d[u]);
+                    store8_any<false>(a.dpre, r * a.ld_dpre + col, rest, d);
             }
         }
     }
@@ -206,7 +203,12 @@ template <int ACT>
 cudaError_t launch_bwd_act(const EpiBwdArgs &a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.n + kBwdCols - 1) / kBwdCols), static_cast<unsigned>(a.chunks));
     if (!a.vec) {
-        epilogue_backward_any_kernel<ACT><<<grid, kBwdThreads, 0, stream>>>(a);
+        switch ((a.dout_bf16 ? 2 : 0) | (a.pre_bf16 ? 1 : 0)) {
+            case 0: epilogue_backward_any_kernel<ACT, false, false><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 1: epilogue_backward_any_kernel<ACT, false, true><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            case 2: epilogue_backward_any_kernel<ACT, true, false><<<grid, kBwdThreads, 0, stream>>>(a); break;
+            default: epilogue_backward_any_kernel<ACT, true, true><<<grid, kBwdThreads, 0, stream>>>(a); break;
+        }
     } else {
         const int types = (a.dout_bf16 ? 4 : 0) | (a.pre_bf16 ? 2 : 0) | (a.dpre_bf16 ? 1 : 0);
         switch (types) {
