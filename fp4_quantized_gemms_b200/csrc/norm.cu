@@ -247,7 +247,7 @@ __device__ __forceinline__ void load8s(const uint8_t *p, int col, int rest, floa
 }
 
 template <int W, int NV, bool SBF16, bool XBF16, bool RES, bool OUT8, bool VEC>
-__global__ void __launch_bounds__(32 * W) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(32 * W, 32 / W) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RingState st;
     __shared__ float s_sum[2][W];
@@ -823,6 +823,7 @@ cudaError_t launch_rmsnorm(const NormArgs &args, cudaStream_t stream) {
             return with_ring_shape(width, [&](auto w) { return launch_fwd_ring<decltype(w)::value>(a, stream); });
     }
     if (width <= 256) return launch_fwd_rows<1, 1>(a, stream);
+    if (width <= 512) return launch_fwd_rows<1, 2>(a, stream);
     if (width <= 1024) return launch_fwd_rows<1, 4>(a, stream);
     // one vector per thread (one token of 8192: 8.0 us with four, 4.3 with one)
     if (width <= 2048) return launch_fwd_rows<8, 1>(a, stream);

@@ -155,6 +155,7 @@ __device__ __forceinline__ void store8_any(void *p, int64_t i, int rest, const f
     const uintptr_t addr = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(i * kSize);
     const int s = static_cast<int>(addr & 15u);           // the same in all lanes
     const int lane = threadIdx.x & 31;
+    if (rest + 8 * lane <= 0) return;                      // nothing for the whole warp
     uint32_t w[4 + kWords];                                // the last 16 bytes of the lane before, then this one's
 #pragma unroll
     for (int k = 0; k < kWords; ++k)
