@@ -438,13 +438,21 @@ ufp4_status_t check_matrix(const void *p, int32_t dtype, int64_t rows, int64_t c
     return elem_aligned(p, dtype) ? UFP4_OK : UFP4_ERR_ALIGNMENT;
 }
 
+// An output in place of an input: allowed when both are the same matrix
+// element for element.
+bool in_place_ok(const void *out, int32_t dt_out, int64_t ld_out, const void *in, int32_t dt_in, int64_t ld_in,
+                 int64_t rows) {
+    return out == nullptr || out != in || (dt_out == dt_in && (rows <= 1 || ld_out == ld_in));
+}
+
 bool act_valid(int32_t act) { return act >= UFP4_ACT_NONE && act <= UFP4_ACT_SILU; }
 
 // Arguments that both passes of the balance loss share.
 ufp4_status_t fill_balance(const void *logits, int64_t ld, int32_t dtype, int64_t tokens, int32_t experts, int32_t topk,
                            const uint8_t *mask, float coef, BalanceArgs *a) {
     if (tokens < 0 || experts < 1 || topk < 1 || coef != coef) return UFP4_ERR_INVALID_ARG;
-    if (experts > kBalanceMaxExperts || tokens > (int64_t(1) << 31) / 2 || topk > kBalanceMaxExperts)
+    if (experts > kBalanceMaxExperts || topk > kBalanceMaxExperts || tokens > (int64_t(1) << 30) ||
+        tokens * topk > (int64_t(1) << 36))     // a block's counts are 32 bits
         return UFP4_ERR_UNSUPPORTED;
     const ufp4_status_t s = check_matrix(logits, dtype, tokens, experts, ld);
     if (s != UFP4_OK) return s;
@@ -896,6 +904,10 @@ ufp4_status_t ufp4_gemm_epilogue(const ufp4_qtensor_t *a, const ufp4_qtensor_t *
             e.pre_bf16 = epi->pre_dtype == UFP4_DTYPE_BF16;
             e.vec_pre = row_vec(epi->pre, epi->pre_dtype, epi->ld_pre, 4);
         }
+        if (m > 0 && n > 0 &&
+            (!in_place_ok(out_dev, out_dtype, ldo, epi->residual, epi->residual_dtype, epi->ld_residual, m) ||
+             epi->pre == out_dev || (epi->pre != nullptr && epi->pre == epi->residual)))
+            return UFP4_ERR_INVALID_ARG;
     }
     return run_gemm(a, b, nullptr, 0, nullptr, 0, m, n, stream, &e);
 }
@@ -922,6 +934,9 @@ ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int3
         s = check_matrix(dpre_dev, dpre_dtype, m, n, ld_dpre);
         if (s != UFP4_OK) return s;
     }
+    if (!in_place_ok(dpre_dev, dpre_dtype, ld_dpre, dout_dev, dout_dtype, ld_dout, m) ||
+        (act != UFP4_ACT_NONE && !in_place_ok(dpre_dev, dpre_dtype, ld_dpre, pre_dev, pre_dtype, ld_pre, m)))
+        return UFP4_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (n == 0) return UFP4_OK;
     if (dbias_dev != nullptr) {
@@ -989,6 +1004,10 @@ ufp4_status_t ufp4_rmsnorm(const void *x_dev, int64_t ld_x, int32_t x_dtype, con
     }
     if (rstd_dev != nullptr && !elem_aligned(rstd_dev, UFP4_DTYPE_FP32)) return UFP4_ERR_ALIGNMENT;
     if (rows == 0 || cols == 0) return UFP4_OK;
+    if (!in_place_ok(h_dev, stream_dtype, ld_h, x_dev, x_dtype, ld_x, rows) ||
+        !in_place_ok(h_dev, stream_dtype, ld_h, residual_dev, stream_dtype, ld_residual, rows) ||
+        (y_dev != nullptr && (y_dev == h_dev || y_dev == residual_dev || y_dev == x_dev)))
+        return UFP4_ERR_INVALID_ARG;
     NormArgs a;
     memset(&a, 0, sizeof(a));
     a.x = x_dev;
@@ -1048,6 +1067,9 @@ ufp4_status_t ufp4_rmsnorm_backward(const void *dy_dev, int64_t ld_dy, int32_t d
     }
     s = check_matrix(dx_dev, dx_dtype, rows, cols, ld_dx);
     if (s != UFP4_OK) return s;
+    if (!in_place_ok(dx_dev, dx_dtype, ld_dx, dy_dev, dy_dtype, ld_dy, rows) ||
+        !in_place_ok(dx_dev, dx_dtype, ld_dx, dh_dev, stream_dtype, ld_dh, rows) || (dx_dev != nullptr && dx_dev == h_dev))
+        return UFP4_ERR_INVALID_ARG;
     if (cols == 0) return UFP4_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dweight_dev != nullptr) {
@@ -1134,6 +1156,7 @@ ufp4_status_t ufp4_moe_balance_backward(const void *logits_dev, int64_t ld, int3
     s = check_matrix(dlogits_dev, dtype, tokens, experts, ld_d);
     if (s != UFP4_OK) return s;
     if (counts_dev == nullptr || valid_tokens_dev == nullptr || dloss_dev == nullptr) return UFP4_ERR_INVALID_ARG;
+    if (!in_place_ok(dlogits_dev, dtype, ld_d, logits_dev, dtype, ld, tokens)) return UFP4_ERR_INVALID_ARG;
     if (((reinterpret_cast<uintptr_t>(counts_dev) | reinterpret_cast<uintptr_t>(valid_tokens_dev)) & 7u) ||
         !elem_aligned(dloss_dev, UFP4_DTYPE_FP32))
         return UFP4_ERR_ALIGNMENT;

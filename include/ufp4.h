@@ -430,7 +430,8 @@ ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int3
  *                 rows beyond `rows` are left alone.  It goes straight into
  *                 the GEMMs as their ALONG_COLS operand.
  *   rstd_dev      fp32 [rows], receives r (for the backward pass), or NULL.
- * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (cols > 32768), CUDA. */
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (cols > 32768, a q of another
+ * grid), CUDA. */
 ufp4_status_t ufp4_rmsnorm(const void *x_dev, int64_t ld_x, int32_t x_dtype, const void *residual_dev,
                            int64_t ld_residual, int32_t stream_dtype, const void *weight_dev, int32_t weight_dtype,
                            float eps, int64_t rows, int64_t cols, void *h_dev, int64_t ld_h, void *y_dev,
@@ -468,7 +469,8 @@ ufp4_status_t ufp4_rmsnorm_backward(const void *dy_dev, int64_t ld_dy, int32_t d
  *                used during the call only; calls that may run at the same
  *                time need one each.
  * The sums are added in a fixed order.  Errors: INVALID_ARG, ALIGNMENT,
- * UNSUPPORTED (experts > 1024), CUDA. */
+ * UNSUPPORTED (experts or topk > 1024, tokens > 2^30, tokens * topk > 2^36),
+ * CUDA. */
 size_t ufp4_moe_balance_workspace(int32_t experts);
 ufp4_status_t ufp4_moe_balance(const void *logits_dev, int64_t ld, int32_t dtype, int64_t tokens, int32_t experts,
                                const int32_t *choices_dev, int32_t topk, const uint8_t *mask_dev, float coef,

@@ -92,6 +92,8 @@ def test_gemm_epilogue(L):
     assert call(residual=P + 1, ld_residual=64) == ALIGN
     assert call(pre=P, ld_pre=63) == BAD and call(pre=P, ld_pre=64, pre_dtype=9) == BAD
     assert call(pre=P + 2, ld_pre=64, pre_dtype=1) == ALIGN
+    assert call(residual=P, ld_residual=65) == BAD and call(residual=P, ld_residual=64, residual_dtype=1) == BAD
+    assert call(pre=P, ld_pre=64) == BAD and call(pre=2 * P, ld_pre=64, residual=2 * P, ld_residual=64) == BAD
     assert call(b=_q(rows=64, k=192)) == MISMATCH
     assert L.ufp4_gemm_epilogue(None, b, None, P, 64, 0, None) == BAD
     assert L.ufp4_gemm_epilogue(a, None, None, P, 64, 0, None) == BAD
@@ -109,6 +111,7 @@ def test_epilogue_backward(L):
     assert call(ldd=63) == BAD and call(dd=2) == BAD and call(dpre=2 * P + 1) == ALIGN
     assert call(dpre=None, dbias=None) == BAD and call(dbias=3 * P + 2) == ALIGN
     assert call(work=None) == BAD and call(work=4 * P + 8) == ALIGN
+    assert call(dpre=P, ldd=65) == BAD and call(dpre=P, gd=1) == BAD and call(dout=5 * P, dpre=P, zd=1) == BAD
     assert call(n=0) == OK
     W = L.ufp4_epilogue_backward_workspace
     assert W(0, 64) == 0 and W(64, 0) == 0 and W(1, 64) == 64 * 4
@@ -158,6 +161,8 @@ def test_rmsnorm(L):
     assert call(y=None, q=_q(rows=128, k=64, **E8)) == BAD                     # no elements
     assert call(y=None, q=_q(rows=128, k=64, elems8=4 * P + 4, **E8)) == ALIGN
     assert call(y=None, q=_q(rows=128, k=64, elems8=4 * P, grid=0, **MX)) == UNSUP
+    assert call(h=P, ldh=65) == BAD and call(h=P, xd=1) == BAD and call(h=2 * P, ldh=65) == BAD
+    assert call(y=P) == BAD and call(y=5 * P) == BAD and call(y=2 * P) == BAD
     assert call(rows=0) == OK
 
 
@@ -174,6 +179,7 @@ def test_rmsnorm_backward(L):
     assert call(dx=None) == BAD and call(lddx=63) == BAD and call(dd=2) == BAD
     assert call(dw=7 * P + 2) == ALIGN and call(work=None) == BAD and call(work=8 * P + 4) == ALIGN
     assert call(rows=-1) == BAD and call(cols=40000, ldg=40000, ldh=40000, lddh=40000, lddx=40000) == UNSUP
+    assert call(dx=P, lddx=65) == BAD and call(dx=P, gd=1) == BAD and call(dx=5 * P, dd=1) == BAD and call(dx=2 * P) == BAD
     assert call(cols=0) == OK and call(rows=0, dw=None) == OK
     W = L.ufp4_rmsnorm_backward_workspace
     assert W(0, 64) == 0 and W(5, 0) == 0 and W(1, 2048) == 2048 * 4 and W(1, 64) == 64 * 4
@@ -186,7 +192,7 @@ def test_moe_balance(L):
 
     assert fwd(x=None) == BAD and fwd(ld=63) == BAD and fwd(dt=2) == BAD and fwd(x=P + 1) == ALIGN
     assert fwd(t=-1) == BAD and fwd(e=0) == BAD and fwd(k=0) == BAD and fwd(coef=float("nan")) == BAD
-    assert fwd(e=1025, ld=1025) == UNSUP and fwd(k=1025) == UNSUP and fwd(t=1 << 31) == UNSUP
+    assert fwd(e=1025, ld=1025) == UNSUP and fwd(k=1025) == UNSUP and fwd(t=1 << 31) == UNSUP and fwd(t=1 << 30, k=128) == UNSUP
     assert fwd(c=None) == BAD and fwd(loss=None) == BAD and fwd(counts=None) == BAD and fwd(valid=None) == BAD
     assert fwd(work=None) == BAD and fwd(work=6 * P + 8) == ALIGN
     assert fwd(c=2 * P + 2) == ALIGN and fwd(loss=3 * P + 2) == ALIGN and fwd(counts=4 * P + 4) == ALIGN
@@ -200,7 +206,7 @@ def test_moe_balance(L):
     assert bwd(e=2000, ld=2000, ldd=2000) == UNSUP
     assert bwd(counts=None) == BAD and bwd(valid=None) == BAD and bwd(dl=None) == BAD and bwd(d=None) == BAD
     assert bwd(ldd=63) == BAD and bwd(d=7 * P + 1) == ALIGN and bwd(counts=4 * P + 4) == ALIGN
-    assert bwd(dl=6 * P + 2) == ALIGN and bwd(t=0) == OK
+    assert bwd(dl=6 * P + 2) == ALIGN and bwd(d=P, ldd=65) == BAD and bwd(t=0) == OK
     W = L.ufp4_moe_balance_workspace
     assert W(0) == 0 and W(1025) == 0 and W(64) > 0
 
