@@ -291,11 +291,15 @@ __global__ void __launch_bounds__(kThreads, J <= 16 ? 2 : 1) balance_backward_ke
     const double n = static_cast<double>(*a.valid_tokens_in);
     const float scale = n == 0.0 ? 0.0f
                                  : static_cast<float>(static_cast<double>(*a.dloss) * a.coef * E / (n * n * a.topk));
+    // g relative to the mean count's (p sums to 1, so the gradient is the same):
+    // a balanced router's small differences come from whole numbers, not from
+    // the cancellation of large products.
+    const int64_t mean = *a.valid_tokens_in * a.topk / E;
     float ge[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int e = expert_of<G, V>(g, j);
-        ge[j] = e < E ? scale * static_cast<float>(a.counts_in[e]) : 0.0f;
+        ge[j] = e < E ? scale * static_cast<float>(a.counts_in[e] - mean) : 0.0f;
     }
     constexpr int U = kTokensAtOnce<J>;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;

@@ -152,6 +152,29 @@ def test_gradient_against_differences():
         assert abs(float((d.double() * v).sum()) - num) <= 4 * P_REL * size + 1e-9
 
 
+def test_balanced_router():
+    """Counts that are equal have no gradient at all; counts that differ by one
+    have the small gradient of the difference (to fp32 of itself, not of the
+    large terms that cancel in it)."""
+    tokens, e = 4096, 16
+    logits, _ = _case(tokens, e, 1, FP32)
+    choice = (torch.arange(tokens, device="cuda") % e).to(torch.int32)[:, None].contiguous()
+    one = torch.ones(1, device="cuda")
+    loss, counts, valid = ufp4.moe_balance(logits, choice)
+    assert bool((counts == tokens // e).all())
+    assert bool((ufp4.moe_balance_backward(logits, counts, valid, one, topk=1) == 0).all())
+    choice[0] = 1
+    loss, counts, valid = ufp4.moe_balance(logits, choice)
+    d = ufp4.moe_balance_backward(logits, counts, valid, one, topk=1)
+    _ok()
+    want = _expect(logits, choice, 1.0)[3]
+    p = torch.softmax(logits.double(), 1)
+    # terms: p (g_e - sum p g) with g = +-1 count, each within P_REL of its size
+    unit = e / float(tokens) ** 2
+    size = p * unit * ((torch.arange(e, device="cuda") < 2).double() + p[:, :2].sum(1, keepdim=True))
+    assert bool(((d.double() - want).abs() <= 2 * P_REL * size + half_step(FP32) * want.abs()).all())
+
+
 def test_in_place_same_bits_streams_and_graph():
     logits, choice = _case(5000, 64, 6, FP32)
     one = torch.ones(1, device="cuda")
