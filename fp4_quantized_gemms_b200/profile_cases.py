@@ -10,6 +10,10 @@ the launch to capture.
     python -m fp4_quantized_gemms_b200.profile_cases quantize --rows 8192 --cols 8192 --axis rows --sr
     python -m fp4_quantized_gemms_b200.profile_cases quantize --rows 8192 --cols 2048 --dual
     python -m fp4_quantized_gemms_b200.profile_cases stats --rows 8192 --cols 8192 --axis rows
+    python -m fp4_quantized_gemms_b200.profile_cases epilogue --m 8192 --n 8192 --k 2048
+    python -m fp4_quantized_gemms_b200.profile_cases norm --rows 16384 --cols 8192
+    python -m fp4_quantized_gemms_b200.profile_cases router --tokens 131072 --experts 256
+    python -m fp4_quantized_gemms_b200.profile_cases clip --elements 100000000
 """
 from __future__ import annotations
 
@@ -104,6 +108,60 @@ def stats_case(rows: int, cols: int, axis: int) -> None:
         raise RuntimeError("device error word set")
 
 
+def _randn(*shape, std=1.0, dtype=torch.bfloat16):
+    return (torch.randn(*shape, device="cuda") * std).to(dtype)
+
+
+def _done() -> None:
+    torch.cuda.synchronize()
+    if ufp4.check_device_status() != ufp4.OK:
+        raise RuntimeError("device error word set")
+
+
+def epilogue_case(m: int, n: int, k: int) -> None:
+    """8-bit activations x 4-bit weights with GELU, bias and the stored
+    pre-activation, and the epilogue's backward pass, twice."""
+    q = ufp4.empty_qtensor(m, k, ufp4.CFG_8BIT)
+    ufp4.rmsnorm(_randn(m, k), _randn(k), q=q)
+    w = ufp4.rht_quantize(_randn(n, k, std=0.02), ufp4.ALONG_COLS,
+                          ufp4.QuantConfig(block=32, scale_fmt=ufp4.SCALE_UE8M0, hadamard_n=0))
+    bias, pre = _randn(n), torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):
+        out = ufp4.gemm_epilogue(q, w, bias=bias, act=ufp4.ACT_GELU, pre=pre)
+        ufp4.epilogue_backward(out, pre, ufp4.ACT_GELU)
+    _done()
+
+
+def norm_case(rows: int, cols: int) -> None:
+    """Norm of x + residual into an 8-bit operand, and its backward pass, twice."""
+    x, res, w, dy = _randn(rows, cols), _randn(rows, cols), _randn(cols), _randn(rows, cols)
+    q = ufp4.empty_qtensor(rows, cols, ufp4.CFG_8BIT)
+    for _ in range(2):
+        _, _, h, rstd = ufp4.rmsnorm(x, w, residual=res, q=q)
+        ufp4.rmsnorm_backward(dy, h, w, rstd, dh=res)
+    _done()
+
+
+def router_case(tokens: int, experts: int, topk: int) -> None:
+    """Balance loss and its gradient on fp32 logits, twice."""
+    logits = _randn(tokens, experts, dtype=torch.float32)
+    choice = torch.topk(logits, topk, dim=1).indices.to(torch.int32)
+    one = torch.ones(1, device="cuda")
+    for _ in range(2):
+        _, counts, valid = ufp4.moe_balance(logits, choice)
+        ufp4.moe_balance_backward(logits, counts, valid, one, topk=topk)
+    _done()
+
+
+def clip_case(elements: int) -> None:
+    """Global norm and clipping of eight fp32 gradients into bf16, twice."""
+    grads = [_randn(elements // 8, dtype=torch.float32) for _ in range(8)]
+    out = [torch.empty_like(g, dtype=torch.bfloat16) for g in grads]
+    for _ in range(2):
+        ufp4.grad_clip(grads, 1.0, out=out)
+    _done()
+
+
 def main() -> None:
     ap = argparse.ArgumentParser()
     sub = ap.add_subparsers(dest="case", required=True)
@@ -131,12 +189,33 @@ def main() -> None:
     t.add_argument("--rows", type=int, default=8192)
     t.add_argument("--cols", type=int, default=8192)
     t.add_argument("--axis", choices=["cols", "rows"], default="rows")
+    e = sub.add_parser("epilogue")
+    e.add_argument("--m", type=int, default=8192)
+    e.add_argument("--n", type=int, default=8192)
+    e.add_argument("--k", type=int, default=2048)
+    n = sub.add_parser("norm")
+    n.add_argument("--rows", type=int, default=16384)
+    n.add_argument("--cols", type=int, default=8192)
+    r = sub.add_parser("router")
+    r.add_argument("--tokens", type=int, default=131072)
+    r.add_argument("--experts", type=int, default=256)
+    r.add_argument("--topk", type=int, default=8)
+    c = sub.add_parser("clip")
+    c.add_argument("--elements", type=int, default=100_000_000)
     a = ap.parse_args()
     if a.case == "gemm":
         gemm_case(a.m, a.n, a.k, ufp4.GRID_E1M2 if a.grid == "e1m2" else ufp4.GRID_E2M1, a.path, a.mx,
                   a.fp32_scales)
     elif a.case == "grouped":
         grouped_case(a.tokens, a.experts, a.hidden, a.ffn)
+    elif a.case == "epilogue":
+        epilogue_case(a.m, a.n, a.k)
+    elif a.case == "norm":
+        norm_case(a.rows, a.cols)
+    elif a.case == "router":
+        router_case(a.tokens, a.experts, a.topk)
+    elif a.case == "clip":
+        clip_case(a.elements)
     elif a.case == "stats":
         stats_case(a.rows, a.cols, ufp4.ALONG_COLS if a.axis == "cols" else ufp4.ALONG_ROWS)
     else:
