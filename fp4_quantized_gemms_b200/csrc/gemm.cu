@@ -2009,25 +2009,31 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
             bool ok = true;
             // The tile's bias as fp32: every epilogue warp writes the columns
             // that it reads (the same values as its neighbours), in two
-            // buffers in turn: a warp is at most one tile ahead of another
-            // that still reads (the accumulator is full only after all have
-            // emptied it).  The first residual piece starts its way now.
+            // buffers in turn.  It is fetched now and written once the
+            // accumulator is full: every warp has emptied the one before by
+            // then, so none still reads the buffer of two tiles ago.  The
+            // first residual piece starts its way now, too.
             float *bias_s = reinterpret_cast<float *>(smem + C::o_bias) + 256 * (tcount & 1);
+            float4 bias_v[kHalves];
             if constexpr (EPI) {
 #pragma unroll
                 for (int hh = 0; hh < kHalves; ++hh) {
-                    const int col = 128 * (h0 + hh) + 4 * lane;
-                    const int64_t left = tl.g.n - (tl.n0 + col);
-                    const int valid = left < 0 ? 0 : left < 4 ? static_cast<int>(left) : 4;
-                    *reinterpret_cast<float4 *>(bias_s + col) = epilogue_bias(args.epi, tl.n0 + col, valid);
+                    const int64_t col = tl.n0 + 128 * (h0 + hh) + 4 * lane;
+                    const int64_t left = tl.g.n - col;
+                    bias_v[hh] = epilogue_bias(args.epi, col, left < 0 ? 0 : left < 4 ? static_cast<int>(left) : 4);
                 }
-                __syncwarp();
             }
             if (EPI && args.epi.tma && args.epi.residual != nullptr && m0 < tl.g.m && tl.n0 + 128 * h0 < tl.g.n) {
                 if (lane == 0) bulk_wait_read<0>();
                 epi_load_residual(args, ew, lane, 0, tl.n0 + 128 * h0, m0);
             }
             if (!warp_wait(acc_full, tcount & 1, kErrTimeoutEpilogue, abort_flag)) break;
+            if constexpr (EPI) {
+#pragma unroll
+                for (int hh = 0; hh < kHalves; ++hh)
+                    *reinterpret_cast<float4 *>(bias_s + 128 * (h0 + hh) + 4 * lane) = bias_v[hh];
+                __syncwarp();
+            }
             tc_fence_after();
             const bool vec_tile = args.c_vec && (tl.g.c_col & 3) == 0;
             const bool zero = tl.g.k == 0;             // no MMA wrote the accumulator
