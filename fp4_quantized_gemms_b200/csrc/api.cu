@@ -606,7 +606,7 @@ using namespace ufp4;
 
 extern "C" {
 
-int32_t ufp4_version(void) { return 100; }
+int32_t ufp4_version(void) { return 200; }
 
 const char *ufp4_status_string(ufp4_status_t s) {
     switch (s) {

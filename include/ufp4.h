@@ -40,6 +40,10 @@
  *     returns an error status and enqueues nothing.
  *   - Inputs are assumed finite; NaN/Inf inputs give unspecified codes.
  *   - Outputs are overwritten (no accumulation into C).
+ *   - ufp4_rmsnorm, ufp4_rmsnorm_backward and ufp4_epilogue_backward read rows
+ *     that are not 16-byte aligned in whole 16-byte units: other bytes of a
+ *     unit that holds an element of a row may be read (and are not used).
+ *     Nothing outside the rows is ever written.
  *
  * Quantized operand layout (ufp4_qtensor_t), for `rows` output rows and
  * reduction length `k`:
