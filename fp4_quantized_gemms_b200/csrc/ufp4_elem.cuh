@@ -322,17 +322,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // Derivative of the activation, two at a time.  With t = exp(-2u) (GELU) or exp(-z) (SiLU)
-// and s = 1 / (1 + t): d = s + z u2' s (t s), where t s = 1 - s without
-// cancellation and u2' = d(2u)/dz.  Beyond |z| = 9 (GELU) or 60 (SiLU) the
-// derivative is 0 or 1 to fp32; the clamp keeps t finite and every product in
-// range.
+// and s = 1 / (1 + t): d = s + z u2' (t s) s, where t s = 1 - s without
+// cancellation and u2' = d(2u)/dz.  (t s first: it is at most 1 and s a normal
+// number, while s^2 would underflow left of z = -43.)  The clamp, |z| = 9.9
+// (GELU) or 87 (SiLU), keeps t finite and s normal; beyond it the derivative is
+// within 3e-35 of 0 or 1.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
     if constexpr (ACT == UFP4_ACT_RELU) {
         return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
     } else if constexpr (ACT == UFP4_ACT_GELU || ACT == UFP4_ACT_SILU) {
         constexpr bool kGelu = ACT == UFP4_ACT_GELU;
-        const float lim = kGelu ? 9.0f : 60.0f;
+        const float lim = kGelu ? 9.9f : 87.0f;
         const float2 c = make_float2(clamp_nan(z.x, lim), clamp_nan(z.y, lim));
         float2 arg, du = c;                              // log2 t; z d(2u)/dz
         if constexpr (kGelu) {
@@ -345,7 +346,7 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         const float2 t = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
         const float2 d = add2(splat(1.0f), t);
         const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-        return fma2(du, mul2(t, mul2(s, s)), s);
+        return fma2(du, mul2(mul2(t, s), s), s);
     } else if constexpr (ACT == UFP4_ACT_GELU_ERF) {
         auto one = [](float v) {
             const float c = clamp_nan(v, 9.0f);

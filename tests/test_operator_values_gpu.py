@@ -1,0 +1,55 @@
+"""Values at the ends of the operators' ranges."""
+import math
+
+import pytest
+import torch
+
+from fp4_quantized_gemms_b200 import ufp4
+from tests.gpu_util import needs_gpu
+from tests.op_util import ACTS
+
+pytestmark = needs_gpu
+
+LOG2E = math.log2(math.e)
+U = 2.0 ** -24
+
+
+def _ok():
+    torch.cuda.synchronize()
+    assert ufp4.check_device_status() == ufp4.OK
+
+
+def _terms(z, act):
+    """(Phi, z Phi', A) of act = z Phi(z) in 64 bits, without cancellation on
+    the left, and A = |log2| of the exponential that the kernels take."""
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return s, z * s * torch.sigmoid(-z), z.abs() * LOG2E
+    a = 2 * math.sqrt(2 / math.pi)
+    u = a * (z + 0.044715 * z ** 3)
+    s = torch.sigmoid(u)
+    return s, z * s * torch.sigmoid(-u) * a * (1 + 3 * 0.044715 * z * z), u.abs() * LOG2E
+
+
+# The exponential's argument takes at most five roundings (its constants'
+# among them), each 2^-24 of it, so ln 2 times that of the result; the
+# exponential and reciprocal themselves (2^-22 and 2^-23) and the rest of the
+# arithmetic are at most 24 roundings more.
+def _relative(a):
+    return (5 * math.log(2) * a + 24) * U
+
+
+# left of these bounds 1 + exp leaves fp32
+LEFT = {"silu": -86.0, "gelu": -9.8}
+
+
+@pytest.mark.parametrize("n", [4096, 4099])
+@pytest.mark.parametrize("act,near", [("silu", -20.0), ("gelu", -5.0)])
+def test_slopes_far_left(act, near, n):
+    """The slope keeps its sign and its relative accuracy where it is tiny."""
+    z = torch.linspace(LEFT[act], near, n, device="cuda").view(1, n)
+    d, _ = ufp4.epilogue_backward(torch.ones_like(z), z, ACTS[act], dpre=torch.empty_like(z), want_dbias=False)
+    _ok()
+    p, q, a = _terms(z.double(), act)
+    assert bool(((d.double() - (p + q)).abs() <= _relative(a) * (p.abs() + q.abs())).all())
+    assert bool((d < 0).all())
