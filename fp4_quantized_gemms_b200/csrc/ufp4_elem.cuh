@@ -255,9 +255,11 @@ struct Raw8 {
 
 // ---------------------------------------------------------------------------
 // Activations (ufp4_act_t) on the hardware's ex2 and reciprocal (ex2.approx and
-// rcp.approx: 2^-22 and 1 ulp).  The argument's own rounding adds 2^-24 per
-// unit of it to a term that is small whenever the argument is large, so every
-// value below is within a few 1e-7 of max(|z|, 1).
+// rcp.approx: 2^-22 and 1 ulp): every value below is within a few 1e-7 of
+// max(|z|, 1).  Where values get small, far left, they keep a relative accuracy
+// of (5 |x| ln 2 + 24) 2^-24, x the binary logarithm of the exponential (the
+// argument's roundings), 3e-5 at worst; below 2^-126 the exponential's side is
+// flushed to 0.
 
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
@@ -285,16 +287,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2A = 2.0f * 0.79788456080286536f;          // 2 sqrt(2 / pi)
 constexpr float kGelu2B = kGelu2A * 0.044715f;
 
-// erf by Abramowitz and Stegun 7.1.26: within 1.5e-7, in 12 operations.
-__device__ __forceinline__ float erf_approx(float x) {
-    const float a = fabsf(x);
-    const float t = rcp_approx(fmaf(0.3275911f, a, 1.0f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float y = fmaf(-p * t, ex2_approx(-kLog2e * a * a), 1.0f);
-    return copysignf(y, x);
+// The normal distribution's tail beyond a >= 0 as a product e r, so with its
+// relative accuracy wherever it is a normal number: e = exp(-a^2 / 2) and
+// r = erfcx(a / sqrt 2) / 2 = t P(t), t = 1 / (1 + 0.3 a).  P is a polynomial of
+// degree 7 fitted to equal relative error over a in [0, 14] (Lawson's iterated
+// least squares): 1.7e-7, 4.5e-7 in fp32 arithmetic.
+struct NormalTail {
+    float e, r;
+};
+__device__ __forceinline__ NormalTail normal_tail(float a) {
+    const float t = rcp_approx(fmaf(0.3f, a, 1.0f));
+    float p = fmaf(0.03567476198077202f, t, -0.15720301866531372f);
+    p = fmaf(p, t, 0.20635341107845306f);
+    p = fmaf(p, t, -0.05368354544043541f);
+    p = fmaf(p, t, 0.1285615712404251f);
+    p = fmaf(p, t, 0.09991350769996643f);
+    p = fmaf(p, t, 0.1207539513707161f);
+    p = fmaf(p, t, 0.11962930113077164f);
+    return {ex2_approx(-0.5f * kLog2e * a * a), p * t};
 }
 
 __device__ __forceinline__ float act_value(float z, int act) {
@@ -304,7 +314,10 @@ __device__ __forceinline__ float act_value(float z, int act) {
             const float p = fmaf(-kGelu2B * kLog2e, z * z, -kGelu2A * kLog2e);
             return z * rcp_approx(1.0f + ex2_approx(z * p));
         }
-        case UFP4_ACT_GELU_ERF: return 0.5f * z * (1.0f + erf_approx(0.70710678118654752f * z));
+        case UFP4_ACT_GELU_ERF: {
+            const NormalTail n = normal_tail(fabsf(z));
+            return z * (z < 0.0f ? n.e * n.r : fmaf(-n.e, n.r, 1.0f));
+        }
         case UFP4_ACT_SILU: return z * rcp_approx(1.0f + ex2_approx(-kLog2e * z));
         default: return z;
     }
@@ -326,7 +339,9 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 // cancellation and u2' = d(2u)/dz.  (t s first: it is at most 1 and s a normal
 // number, while s^2 would underflow left of z = -43.)  The clamp, |z| = 9.9
 // (GELU) or 87 (SiLU), keeps t finite and s normal; beyond it the derivative is
-// within 3e-35 of 0 or 1.
+// within 3e-35 of 0 or 1.  GELU_ERF: the tail beyond |z| less |z| times the
+// density there (no cancellation but at its zero, |z| = 0.75), or 1 less that;
+// within 2e-36 beyond |z| = 13.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
     if constexpr (ACT == UFP4_ACT_RELU) {
@@ -349,9 +364,10 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         return fma2(du, mul2(mul2(t, s), s), s);
     } else if constexpr (ACT == UFP4_ACT_GELU_ERF) {
         auto one = [](float v) {
-            const float c = clamp_nan(v, 9.0f);
-            return fmaf(c * 0.39894228040143268f, ex2_approx(-0.5f * kLog2e * c * c),
-                        0.5f * (1.0f + erf_approx(0.70710678118654752f * c)));
+            const float c = clamp_nan(v, 13.0f), a = fabsf(c);
+            const NormalTail n = normal_tail(a);
+            const float d = fmaf(-0.39894228040143268f, a, n.r);      // tail and density over e
+            return c < 0.0f ? n.e * d : fmaf(-n.e, d, 1.0f);
         };
         return make_float2(one(z.x), one(z.y));
     } else {

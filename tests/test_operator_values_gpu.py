@@ -6,7 +6,7 @@ import torch
 
 from fp4_quantized_gemms_b200 import ufp4
 from tests.gpu_util import needs_gpu
-from tests.op_util import ACTS
+from tests.op_util import ACTS, BF16, FP32, eight_bit, half_step, rand
 
 pytestmark = needs_gpu
 
@@ -25,10 +25,12 @@ def _terms(z, act):
     if act == "silu":
         s = torch.sigmoid(z)
         return s, z * s * torch.sigmoid(-z), z.abs() * LOG2E
-    a = 2 * math.sqrt(2 / math.pi)
-    u = a * (z + 0.044715 * z ** 3)
-    s = torch.sigmoid(u)
-    return s, z * s * torch.sigmoid(-u) * a * (1 + 3 * 0.044715 * z * z), u.abs() * LOG2E
+    if act == "gelu":
+        a = 2 * math.sqrt(2 / math.pi)
+        u = a * (z + 0.044715 * z ** 3)
+        s = torch.sigmoid(u)
+        return s, z * s * torch.sigmoid(-u) * a * (1 + 3 * 0.044715 * z * z), u.abs() * LOG2E
+    return (0.5 * torch.erfc(-z / math.sqrt(2)), z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi), z * z / 2 * LOG2E)
 
 
 # The exponential's argument takes at most five roundings (its constants'
@@ -39,12 +41,12 @@ def _relative(a):
     return (5 * math.log(2) * a + 24) * U
 
 
-# left of these bounds 1 + exp leaves fp32
-LEFT = {"silu": -86.0, "gelu": -9.8}
+# left of these bounds 1 + exp leaves fp32, or the value its normal numbers
+LEFT = {"silu": -86.0, "gelu": -9.8, "gelu_erf": -12.5}
 
 
 @pytest.mark.parametrize("n", [4096, 4099])
-@pytest.mark.parametrize("act,near", [("silu", -20.0), ("gelu", -5.0)])
+@pytest.mark.parametrize("act,near", [("silu", -20.0), ("gelu", -5.0), ("gelu_erf", -3.0)])
 def test_slopes_far_left(act, near, n):
     """The slope keeps its sign and its relative accuracy where it is tiny."""
     z = torch.linspace(LEFT[act], near, n, device="cuda").view(1, n)
@@ -53,3 +55,21 @@ def test_slopes_far_left(act, near, n):
     p, q, a = _terms(z.double(), act)
     assert bool(((d.double() - (p + q)).abs() <= _relative(a) * (p.abs() + q.abs())).all())
     assert bool((d < 0).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_erf"])
+def test_values_far_left(act):
+    """act(z) itself, from a bias on a product of zeros and without a product."""
+    n = 4096
+    bias = torch.linspace(LEFT[act], 6.0, n, device="cuda")
+    w = eight_bit(rand(1, n, 64, std=0.05).float())
+    zeros = eight_bit(torch.zeros(3, 64, device="cuda"))
+    p, _, a = _terms(bias.double(), act)
+    want = bias.double() * p
+    empty = [ufp4.empty_qtensor(r, 0, w.cfg) for r in (3, n)]
+    for q in ((zeros, w), empty):
+        y = ufp4.gemm_epilogue(*q, bias=bias, act=ACTS[act], out_dtype=FP32)
+        yb = ufp4.gemm_epilogue(*q, bias=bias, act=ACTS[act])
+        _ok()
+        assert bool(((y.double() - want).abs() <= _relative(a) * want.abs()).all())
+        assert bool(((yb.double() - want).abs() <= (_relative(a) + half_step(BF16)) * 1.001 * want.abs()).all())
