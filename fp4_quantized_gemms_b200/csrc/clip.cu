@@ -8,9 +8,11 @@
 // HBM bounds both.  The second pass visits the chunks in the opposite order:
 // what the first one read last is still in L2.
 //
-// Squares are added in fp32 eight at a time and then in fp64; where eight
-// squares leave fp32's comfortable range they are taken in fp64, so gradients
-// of any size have an exact norm.
+// Squares are added in fp32 eight at a time and then in fp64 (so the norm is
+// within 6 * 2^-24 of its value); where eight squares leave fp32's comfortable
+// range they are taken in fp64, so this holds for gradients of any size.  The
+// factor max_norm / N is fp32; below fp32's normal numbers, where it would lose
+// bits that the products still have, it stays fp64 and so do the products.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -142,7 +144,9 @@ __global__ void __launch_bounds__(kThreads)
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(n);
     // A norm that is not finite leaves the values as they are.
     const bool scale = n > static_cast<double>(max_norm) && n < static_cast<double>(CUDART_INF);
-    const float coef = scale ? static_cast<float>(static_cast<double>(max_norm) / n) : 1.0f;
+    const double ratio = scale ? static_cast<double>(max_norm) / n : 1.0;
+    const float coef = static_cast<float>(ratio);
+    const bool tiny = ratio < 1.1754943508222875e-38 && ratio > 0.0;      // 2^-126
     for (int64_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
         const int64_t c = t.chunks - 1 - k;
         const ClipEntry &e = t.e[tensor_of(t, c)];
@@ -154,7 +158,10 @@ __global__ void __launch_bounds__(kThreads)
             const int valid = static_cast<int>(end - i < 8 ? end - i : 8);
             float v[8];
             get8(e.src, i, e.src_bf16, e.vec, valid, v);
-            if (scale) {
+            if (tiny) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(v[j] * ratio);
+            } else if (scale) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] *= coef;
             }

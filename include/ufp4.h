@@ -504,7 +504,9 @@ typedef struct {
 } ufp4_tensor_t;
 
 /* Global norm of many gradients, N = sqrt(sum of all squares) (fp64 inside),
- * and clipping: dst = src * min(1, max_norm / N), rounded once.
+ * and clipping: dst = src * min(1, max_norm / N) in fp32 (the factor and the
+ * product are rounded; a factor below 2^-126 is applied in fp64), then rounded
+ * to dst's type.
  *   tensors_host  array of n_tensors in host memory, read before the call
  *                 returns (a captured call keeps the addresses it saw).
  *   norm_dev      fp32, receives N.

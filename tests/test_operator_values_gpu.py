@@ -73,3 +73,21 @@ def test_values_far_left(act):
         _ok()
         assert bool(((y.double() - want).abs() <= _relative(a) * want.abs()).all())
         assert bool(((yb.double() - want).abs() <= (_relative(a) + half_step(BF16)) * 1.001 * want.abs()).all())
+
+
+@pytest.mark.parametrize("dst", [None, FP32, BF16])
+@pytest.mark.parametrize("max_norm", [1e-4, 1e-8, 1e-20, 1e-38])
+def test_clip_by_a_tiny_factor(max_norm, dst):
+    """max_norm / N below fp32's normal numbers: the product need not be."""
+    ts = [rand(1, 1003, dtype=FP32) * 3e36, rand(2, 64, dtype=FP32) * 1e20, rand(3, 520) * 1e36]
+    before = [t.double() for t in ts]
+    out = [torch.empty(t.numel(), dtype=dst, device="cuda") for t in ts] if dst else None
+    ufp4.grad_clip(ts, max_norm, out=out)
+    _ok()
+    m = float(torch.tensor(max_norm, dtype=FP32))            # as the call takes it
+    c = m / math.sqrt(sum(float(t.square().sum()) for t in before))
+    for o, b in zip(out or ts, before):
+        want = b * c
+        # the norm's and the factor's roundings, one to the type, and its smallest step
+        lim = (half_step(o.dtype) * 1.001 + 8 * U) * want.abs() + 2.0 ** -150 + (2.0 ** -134 if o.dtype == BF16 else 0)
+        assert bool(((o.double() - want).abs() <= lim).all())
