@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <iterator>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -481,16 +482,28 @@ ufp4_status_t check_tensors(const ufp4_tensor_t *t, int32_t n, bool clip) {
             return UFP4_ERR_ALIGNMENT;
         if (clip && t[i].dst == t[i].src && t[i].dst_dtype != t[i].src_dtype) return UFP4_ERR_INVALID_ARG;
     }
-    if (clip) {   // destinations that overlap (the same tensor listed twice) would be scaled twice
-        std::vector<std::pair<uintptr_t, uintptr_t>> r;
+    if (clip) {
+        // Destinations that overlap (the same tensor listed twice) would be
+        // scaled twice, and a source that a destination overlaps (in any other
+        // way than by being it) would be read scaled or half written.
+        using Range = std::pair<uintptr_t, uintptr_t>;
+        auto range = [](const void *p, int64_t len, int32_t dtype) {
+            const uintptr_t d = reinterpret_cast<uintptr_t>(p);
+            return Range(d, d + static_cast<uintptr_t>(len) * elem_bytes(dtype));
+        };
+        std::vector<Range> r;
         r.reserve(static_cast<size_t>(n));
-        for (int32_t i = 0; i < n; ++i) {
-            const uintptr_t d = reinterpret_cast<uintptr_t>(t[i].dst);
-            if (t[i].n > 0) r.emplace_back(d, d + static_cast<uintptr_t>(t[i].n) * elem_bytes(t[i].dst_dtype));
-        }
+        for (int32_t i = 0; i < n; ++i)
+            if (t[i].n > 0) r.push_back(range(t[i].dst, t[i].n, t[i].dst_dtype));
         std::sort(r.begin(), r.end());
         for (size_t i = 1; i < r.size(); ++i)
             if (r[i].first < r[i - 1].second) return UFP4_ERR_INVALID_ARG;
+        for (int32_t i = 0; i < n; ++i) {
+            if (t[i].n == 0 || t[i].dst == t[i].src) continue;      // in place: the loop above has looked
+            const Range s = range(t[i].src, t[i].n, t[i].src_dtype);
+            const auto next = std::lower_bound(r.begin(), r.end(), Range(s.second, 0));   // first at or behind its end
+            if (next != r.begin() && std::prev(next)->second > s.first) return UFP4_ERR_INVALID_ARG;
+        }
     }
     return UFP4_OK;
 }

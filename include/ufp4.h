@@ -516,8 +516,9 @@ typedef struct {
  * A NaN or an infinity among the gradients makes N NaN or infinite; then
  * nothing is scaled (dst = src).  (A finite N beyond fp32's range is reported
  * as infinity, and the gradients are scaled by it.)  The sums are added in a
- * fixed order.  Errors: INVALID_ARG (a negative or NaN max_norm, two
- * destinations that overlap, among others), ALIGNMENT, CUDA. */
+ * fixed order.  Errors: INVALID_ARG (a negative or NaN max_norm, a
+ * destination that overlaps another one or any source but its own, among
+ * others), ALIGNMENT, CUDA. */
 size_t ufp4_grad_norm_workspace(int32_t n_tensors);
 ufp4_status_t ufp4_grad_norm(const ufp4_tensor_t *tensors_host, int32_t n_tensors, float *norm_dev,
                              void *workspace_dev, void *stream);

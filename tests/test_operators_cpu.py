@@ -233,3 +233,22 @@ def test_grad_clip(L):
     assert L.ufp4_grad_norm(table((4 * P + 1, None, 10, 0, 0)), 1, P, 2 * P, None) == ALIGN
     W = L.ufp4_grad_norm_workspace
     assert W(0) == W(1) == W(512) and W(513) == 2 * W(1) and W(1) % 8 == 0
+
+
+def test_grad_clip_overlapping_sources(L):
+    """A destination may be its own source, and overlaps no other tensor."""
+    def clip(*rows):
+        return L.ufp4_grad_clip((ufp4.TensorC * len(rows))(*[ufp4.TensorC(*r) for r in rows]), len(rows), 1.0, P, 2 * P, None)
+
+    a, b, c = 4 * P, 5 * P, 6 * P
+    for bad in ([(a, b, 100, 1, 1), (b, a, 100, 1, 1)],                      # exchanged
+                [(a, c, 100, 1, 1), (b, a, 100, 1, 1)],                      # another's source
+                [(b, a, 100, 1, 1), (a, a + 400, 100, 1, 1)],                # the same, in the other order
+                [(a, a, 100, 1, 1), (a, c, 100, 1, 1)],                      # read by one, in place in the other
+                [(a, a + 4, 100, 1, 1)], [(a + 4, a, 100, 1, 1)],            # its own source, shifted
+                [(a, a + 196, 100, 0, 1)], [(a + 396, a, 100, 1, 1)],
+                [(a, c, 100, 1, 1), (b, a + 396, 100, 1, 1)],                # by one element
+                [(a, c, 100, 1, 1), (b, a - 200, 101, 1, 0)],                # by half of one
+                [(a, c, 10, 1, 1)] * 1 + [(b, c + 4096 + 64 * i, 4, 1, 1) for i in range(600)] + [(b + 4096, a, 1, 1, 0)]):
+        for rows in (bad, bad[::-1]):
+            assert clip(*rows) == BAD, bad[:3]
