@@ -797,8 +797,8 @@ def grad_norm(grads) -> torch.Tensor:
 def grad_clip(grads, max_norm: float, out=None) -> torch.Tensor:
     """Clips a list of gradients to a global norm of max_norm, in place or into
     the tensors of `out` (same sizes, bfloat16 or float32; each overlaps no
-    other tensor of the call); returns the norm before clipping, float32 [1].  A norm that is not finite leaves the values
-    as they are."""
+    other tensor of the call); returns the norm before clipping, float32 [1].
+    A norm that is not finite leaves the values as they are."""
     _need(out is None or len(out) == len(grads), "out: a tensor for each gradient")
     table, device = _tensor_table(grads, out)
     norm = grads[0].new_empty(1, dtype=torch.float32)
