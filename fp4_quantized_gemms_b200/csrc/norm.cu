@@ -12,7 +12,8 @@
 // One pass: a row is read once, held in registers while its sum is reduced,
 // and written once, so HBM is the bound (forward 7 bytes per element for a
 // bf16 stream with residual and 8-bit output, backward 8).  Row sums, r and
-// the weight gradient are fp32.
+// the weight gradient are fp32.  The forward mean divides: with a rounded
+// 1 / cols elements crossed borders of the 8-bit rounding.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(32 * W, 32 / W) rmsnorm_ring_kernel(const __gr
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[j][e] = make_float2(v[2 * e], v[2 * e + 1]);
     }
-    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    const float count = static_cast<float>(a.cols);
     int s = 0;
     uint32_t parity = 0;
     bool bad = false;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(32 * W, 32 / W) rmsnorm_ring_kernel(const __gr
         sum = row_sum<W>(sum, s_sum[k & 1], &bad);
         if (bad) break;
         if (t == 0 && k + a.stages < n) issue(k + a.stages);
-        const float rstd = 1.0f / sqrtf(sum * inv_cols + a.eps);
+        const float rstd = 1.0f / sqrtf(sum / count + a.eps);
         if (t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
         const RowFactors factors(a, row);
 #pragma unroll
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(RowShape<W>::kThreads) rmsnorm_kernel(const __
         for (int e = 0; e < 8; ++e) sum = fmaf(h[j][e], h[j][e], sum);
     }
     sum = row_sum<W>(sum, s_sum);
-    const float rstd = 1.0f / sqrtf(sum * (1.0f / static_cast<float>(a.cols)) + a.eps);
+    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
     if (t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
     const RowFactors factors(a, row);
 #pragma unroll

@@ -1,4 +1,5 @@
-"""Values at the ends of the operators' ranges."""
+"""Values at the ends of the operators' ranges, and norms that have an exact
+value."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 from fp4_quantized_gemms_b200 import ufp4
 from tests.gpu_util import needs_gpu
-from tests.op_util import ACTS, BF16, FP32, eight_bit, half_step, rand
+from tests.op_util import ACTS, BF16, FP32, eight_bit, half_step, rand, values64
 
 pytestmark = needs_gpu
 
@@ -91,3 +92,17 @@ def test_clip_by_a_tiny_factor(max_norm, dst):
         # the norm's and the factor's roundings, one to the type, and its smallest step
         lim = (half_step(o.dtype) * 1.001 + 8 * U) * want.abs() + 2.0 ** -150 + (2.0 ** -134 if o.dtype == BF16 else 0)
         assert bool(((o.double() - want).abs() <= lim).all())
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_norm_of_ones(rows):
+    """The mean of ones is 1 at every width: rstd is 1, and with a weight of
+    1.0625, half way between two 8-bit values, the even one is taken."""
+    for cols in [*range(1, 300), 999, 1000, 1025, 1409, 2047, 4099, 8191, 12345, 16383, 32761]:
+        x = torch.ones(rows, cols, dtype=BF16, device="cuda")
+        w = torch.full((cols,), 1.0625, device="cuda")
+        q = ufp4.empty_qtensor(rows, cols, ufp4.CFG_8BIT)
+        _, _, _, rstd = ufp4.rmsnorm(x, w, eps=0.0, q=q)
+        assert bool((rstd == 1).all()), cols
+        assert bool((values64(q)[:, :cols] == 1).all()), cols
+    _ok()
