@@ -170,7 +170,14 @@ __device__ __forceinline__ void write_y(const NormArgs &a, const RowFactors &f, 
     if constexpr (!OUT8) {
         put8<true, VEC>(a.y, row * a.ld_y + col, rest, v);
     } else {
-        float amax = max_abs3(max_abs3(max_abs3(v[0], v[1], v[2]), v[3], v[4]), max_abs3(v[5], v[6], v[7]), 0.0f);
+        float u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = v[e];
+        if (rest < 8) {                                   // padding: 0 in rows that are not finite, too
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = e < rest ? u[e] : 0.0f;
+        }
+        float amax = max_abs3(max_abs3(max_abs3(u[0], u[1], u[2]), u[3], u[4]), max_abs3(u[5], u[6], u[7]), 0.0f);
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
         const int x = block_exponent(amax);
@@ -179,7 +186,7 @@ __device__ __forceinline__ void write_y(const NormArgs &a, const RowFactors &f, 
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                p[e] = __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[2 * e], v[2 * e + 1]), splat(inv)), __NV_SATFINITE,
+                p[e] = __nv_cvt_float2_to_fp8x2(mul2(make_float2(u[2 * e], u[2 * e + 1]), splat(inv)), __NV_SATFINITE,
                                                 __NV_E4M3);
             *reinterpret_cast<uint2 *>(a.elems8 + row * a.kpad + col) =
                 make_uint2(plain_zeros(p[0] | (p[1] << 16)), plain_zeros(p[2] | (p[3] << 16)));

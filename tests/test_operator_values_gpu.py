@@ -106,3 +106,15 @@ def test_norm_of_ones(rows):
         assert bool((rstd == 1).all()), cols
         assert bool((values64(q)[:, :cols] == 1).all()), cols
     _ok()
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 200), (5, 1990), (300, 1500), (300, 5001)])
+def test_padding_of_rows_that_are_not_finite(rows, cols):
+    """Elements behind the row are 0 whatever the row holds."""
+    x, w = rand(1, rows, cols), rand(2, cols)
+    x[1, 3], x[2, 5], x[4] = float("nan"), float("inf"), 0
+    q = ufp4.empty_qtensor(rows, cols, ufp4.CFG_8BIT)
+    q.elems8.fill_(0x55)
+    ufp4.rmsnorm(x, w, eps=0.0, q=q)
+    _ok()
+    assert q.kpad > cols and bool((q.elems8[:, cols:] == 0).all())
