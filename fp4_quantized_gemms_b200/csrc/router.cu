@@ -283,14 +283,35 @@ __global__ void __cluster_dims__(kFinishBlocks) __launch_bounds__(1024)
     cluster.sync();         // the other blocks' sums stay until they are read
 }
 
+// dloss coef E / (k T^2), what makes g of a count.
+__device__ __forceinline__ float balance_scale(const BalanceArgs &a) {
+    const double n = static_cast<double>(*a.valid_tokens_in);
+    return n == 0.0 ? 0.0f
+                    : static_cast<float>(static_cast<double>(*a.dloss) * a.coef * a.experts / (n * n * a.topk));
+}
+
+// Tokens that do not count have p = 0, and 0 (g - dot) is 0 unless g is not
+// finite: then their zeros are written once more, by the lanes that stored
+// there.  (A choice in the backward kernel's loop, or this inlined behind it,
+// cost 256 bf16 experts 5 to 15%.)
+template <int G, int J, int V, bool BF16>
+__device__ __noinline__ void zero_masked(const BalanceArgs &a) {
+    if (a.mask == nullptr || fabsf(balance_scale(a)) < 1e25f) return;      // |g| <= 2^36 scale
+    const int64_t groups = kThreads / G;
+    for (int64_t t = blockIdx.x * groups + threadIdx.x / G; t < a.tokens; t += gridDim.x * groups) {
+        for (int j = 0; j < J && a.mask[t] == 0; ++j) {
+            const int e = expert_of<G, V>(threadIdx.x % G, j);
+            if (e < a.experts) store_elem(a.dlogits, t * a.ld_d + e, BF16, 0.0f);
+        }
+    }
+}
+
 template <int G, int J, int V, bool BF16>
 __global__ void __launch_bounds__(kThreads, J <= 16 ? 2 : 1) balance_backward_kernel(const __grid_constant__ BalanceArgs a) {
     constexpr int kGroups = kThreads / G;
     const int g = threadIdx.x % G;
     const int E = a.experts;
-    const double n = static_cast<double>(*a.valid_tokens_in);
-    const float scale = n == 0.0 ? 0.0f
-                                 : static_cast<float>(static_cast<double>(*a.dloss) * a.coef * E / (n * n * a.topk));
+    const float scale = balance_scale(a);
     // g relative to the mean count's (p sums to 1, so the gradient is the same):
     // a balanced router's small differences come from whole numbers, not from
     // the cancellation of large products.
@@ -339,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, J <= 16 ? 2 : 1) balance_backward_ke
             }
         }
     }
+    zero_masked<G, J, V, BF16>(a);
 }
 
 template <int G, int J, int V, bool BF16>

@@ -1,5 +1,6 @@
-"""Values at the ends of the operators' ranges, and norms that have an exact
-value."""
+"""Values at the ends of the operators' ranges: activations and slopes far from
+zero, clipping factors below fp32's normal range, norms that have an exact
+value, what stays 0 beside values that are not finite."""
 import math
 
 import pytest
@@ -118,3 +119,17 @@ def test_padding_of_rows_that_are_not_finite(rows, cols):
     ufp4.rmsnorm(x, w, eps=0.0, q=q)
     _ok()
     assert q.kpad > cols and bool((q.elems8[:, cols:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("e", [8, 24, 255, 256, 1000])
+@pytest.mark.parametrize("dloss", [float("inf"), float("nan")])
+def test_masked_tokens_stay_zero(e, dloss, dtype):
+    """A loss gradient that is not finite reaches the tokens that count alone."""
+    logits = rand(1, 300, e, dtype=dtype)
+    choice = torch.topk(logits.float(), 2, dim=1).indices.to(torch.int32)
+    mask = torch.arange(300, device="cuda") % 3 != 0
+    _, counts, valid = ufp4.moe_balance(logits, choice, mask=mask)
+    d = ufp4.moe_balance_backward(logits, counts, valid, torch.full((1,), dloss, device="cuda"), topk=2, mask=mask)
+    _ok()
+    assert bool((d[~mask] == 0).all()) and not bool(d[mask].isfinite().all())
