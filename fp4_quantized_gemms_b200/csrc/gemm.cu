@@ -2066,7 +2066,7 @@ __global__ void __launch_bounds__(PairCfg<GRID, ATOMS, LANES>::kThreads, 1)
                                                   abort_flag);
                         continue;
                     }
-if (m0 < tl.g.m)
+                    if (m0 < tl.g.m)
                         epilogue_rows_any(args.epi, buf, lane, bias_s + 128 * h, m0, tl.n0 + 128 * h, tl.g.m, tl.g.n, r,
                                           mult);
                 } else {

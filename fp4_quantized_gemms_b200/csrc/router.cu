@@ -59,6 +59,13 @@ constexpr int kTokensAtOnce = J <= 4 ? 4 : J <= 16 ? 2 : 1;
 // sum; experts beyond E and tokens that do not count (`live` false) give 0.
 // -inf logits give 0; a row of nothing but -inf gives 0 everywhere.  NaN
 // stays NaN.
+//
+// Fewer bits than expf and a division would give, by choice: ex2.approx is
+// within 2^-22, the product with log2 e within 2^-24 per unit of max - x, and
+// __fdividef within 2 ulp.  At 131072 x 256 fp32 the gradient is 8.7e-8 from 64
+// bits (relative norm); carrying the product's rounding along left that as it is
+// and cost 9% forward, 3% backward (bf16: 16 and 20%), an exact division gave
+// 8.6e-8 and cost 255 experts 3%.
 template <int G, int J, int V, bool BF16, int U>
 __device__ __forceinline__ void token_exp(const BalanceArgs &a, const int64_t (&token)[U], const bool (&live)[U], int g,
                                           float (&p)[U][J], float (&inv)[U]) {
