@@ -1362,8 +1362,13 @@ __device__ __forceinline__ void store_piece(const GemmArgs &args, const Tile &tl
 // with the result.  The copies clip rows and columns outside the matrix (rows
 // are whole 16-byte units, which is where a store clips).  A
 // first form finished four columns of eight rows per lane with ordinary
-// accesses: 20 instructions per element against 11, and 298 against 170 us
-// for the MX product 8192 x 8192 x 2048 with GELU, bias and pre-activation.
+// accesses: 20 instructions per element against 11, and 298 against 176 us
+// for the MX product 8192 x 8192 x 2048 with GELU, bias and pre-activation (165
+// without an epilogue).
+//
+// The kernels spill: 460 bytes a thread with factor atoms, 630 to 660 without
+// (none to 12 without an epilogue), for this path and the any-alignment one
+// below, five activations each, around 128 live accumulators at 168 registers.
 //
 // Buffer: two slots of 2 KB for bf16 pieces (out in turn, or slot 0 out and
 // slot 1 pre), one of 4 KB for fp32 pieces.  16-byte unit u of row r sits at
@@ -1583,8 +1588,8 @@ __device__ __forceinline__ void epi_put(void *p, int64_t ld, bool bf16, uint8_t 
 // buffer by ordinary accesses (MX 8192 x 8191 x 2048 with GELU and bias: 190
 // us; finishing columns of a staged piece, with each element's address and
 // type on the way, took 400).  The four pieces are unrolled: with one copy of
-// this code the 128 accumulators live across it spilled, and the kernel's
-// shared memory leaves too little L1 for that (313 us).
+// this code more of the 128 accumulators live across it spilled, and the
+// kernel's shared memory leaves too little L1 for that (313 us).
 template <int ACT>
 __device__ __forceinline__ void epilogue_pieces_any(const EpiArgs &e, uint8_t *buf, int lane, const float *bias,
                                                     int64_t row0, int64_t col0, int64_t m, int64_t n,

@@ -220,7 +220,9 @@ typedef enum { UFP4_DTYPE_BF16 = 0, UFP4_DTYPE_FP32 = 1 } ufp4_dtype_t;
 /* Activations of the GEMM epilogue:
  *   UFP4_ACT_GELU      z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
  *   UFP4_ACT_GELU_ERF  z (1 + erf(z / sqrt 2)) / 2
- *   UFP4_ACT_SILU      z / (1 + exp(-z)) */
+ *   UFP4_ACT_SILU      z / (1 + exp(-z))
+ * in fp32, within a few 1e-7 of max(|z|, 1); far left of zero, where values
+ * and slopes are small, within 3e-5 of themselves down to about 1e-36. */
 typedef enum {
     UFP4_ACT_NONE = 0,
     UFP4_ACT_RELU = 1,
@@ -232,9 +234,11 @@ typedef enum {
 /* What a GEMM's epilogue does to the product P[M][N]:
  *   z = P + bias;  pre = z;  out = act(z) + residual
  * in fp32, each stored value rounded once.  A NULL pointer leaves that part
- * out.  Pointers are device pointers, element-aligned (rows that are aligned
- * to four elements get vector accesses).  residual may be out itself (the
- * same pointer, type and row pitch); otherwise the tensors may not overlap. */
+ * out.  Pointers are device pointers, element-aligned.  (Fastest: every tensor
+ * 16-byte aligned, rows a whole number of 16-byte units apart and N a whole
+ * number of units long, out, residual and pre all bf16, or out and residual
+ * fp32 without a stored pre.)  residual may be out itself (the same pointer,
+ * type and row pitch); otherwise the tensors may not overlap. */
 typedef struct {
     const void *bias;         /* [N] or NULL                                   */
     const void *residual;     /* [M][ld_residual] or NULL                      */
@@ -406,11 +410,12 @@ ufp4_status_t ufp4_gemm_epilogue(const ufp4_qtensor_t *a, const ufp4_qtensor_t *
  *   dbias[j] = sum_i dout[i][j] * act'(pre[i][j])   (fp32, of the unrounded terms)
  * dL/dresidual is dout itself.  pre is z as ufp4_gemm_epilogue stored it (may
  * be NULL for UFP4_ACT_NONE); relu'(0) = 0.  dpre_dev or dbias_dev may be NULL
- * (not both).  dpre may be dout itself (same pointer, type and pitch).
+ * (not both).  dpre may be dout or pre itself (same pointer, type and pitch).
  * dbias needs workspace_dev of ufp4_epilogue_backward_workspace(m, n) bytes
  * (16-byte aligned), used during the call only; calls that may run at the same
  * time need one each.  The sums are added in a fixed order: the same bits on
- * every call.  Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+ * every call.  Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (m or n > 2^31),
+ * CUDA. */
 size_t ufp4_epilogue_backward_workspace(int64_t m, int64_t n);
 ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int32_t dout_dtype,
                                      const void *pre_dev, int64_t ld_pre, int32_t pre_dtype, int32_t act,
@@ -434,8 +439,8 @@ ufp4_status_t ufp4_epilogue_backward(const void *dout_dev, int64_t ld_dout, int3
  *                 rows beyond `rows` are left alone.  It goes straight into
  *                 the GEMMs as their ALONG_COLS operand.
  *   rstd_dev      fp32 [rows], receives r (for the backward pass), or NULL.
- * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (cols > 32768, a q of another
- * grid), CUDA. */
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (cols > 32768, rows > 2^31 - 4, a
+ * q of another grid), CUDA. */
 ufp4_status_t ufp4_rmsnorm(const void *x_dev, int64_t ld_x, int32_t x_dtype, const void *residual_dev,
                            int64_t ld_residual, int32_t stream_dtype, const void *weight_dev, int32_t weight_dtype,
                            float eps, int64_t rows, int64_t cols, void *h_dev, int64_t ld_h, void *y_dev,
