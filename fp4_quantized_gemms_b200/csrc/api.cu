@@ -13,6 +13,7 @@
 #include <cmath>
 #include <iterator>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -492,7 +493,11 @@ ufp4_status_t check_tensors(const ufp4_tensor_t *t, int32_t n, bool clip) {
             return Range(d, d + static_cast<uintptr_t>(len) * elem_bytes(dtype));
         };
         std::vector<Range> r;
-        r.reserve(static_cast<size_t>(n));
+        try {
+            r.reserve(static_cast<size_t>(n));      // the only allocation
+        } catch (const std::bad_alloc &) {
+            return UFP4_ERR_UNSUPPORTED;
+        }
         for (int32_t i = 0; i < n; ++i)
             if (t[i].n > 0) r.push_back(range(t[i].dst, t[i].n, t[i].dst_dtype));
         std::sort(r.begin(), r.end());

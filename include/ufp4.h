@@ -523,7 +523,8 @@ typedef struct {
  * as infinity, and the gradients are scaled by it.)  The sums are added in a
  * fixed order.  Errors: INVALID_ARG (a negative or NaN max_norm, a
  * destination that overlaps another one or any source but its own, among
- * others), ALIGNMENT, CUDA. */
+ * others), ALIGNMENT, UNSUPPORTED (no host memory to look a list of that length
+ * over: 16 bytes per tensor), CUDA. */
 size_t ufp4_grad_norm_workspace(int32_t n_tensors);
 ufp4_status_t ufp4_grad_norm(const ufp4_tensor_t *tensors_host, int32_t n_tensors, float *norm_dev,
                              void *workspace_dev, void *stream);

@@ -3,6 +3,7 @@ on the host, before any CUDA call (no GPU needed)."""
 import ctypes
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -252,3 +253,25 @@ def test_grad_clip_overlapping_sources(L):
                 [(a, c, 10, 1, 1)] * 1 + [(b, c + 4096 + 64 * i, 4, 1, 1) for i in range(600)] + [(b + 4096, a, 1, 1, 0)]):
         for rows in (bad, bad[::-1]):
             assert clip(*rows) == BAD, bad[:3]
+
+
+def test_grad_clip_without_host_memory(L):
+    """A list too long for the memory that its check needs is refused; no
+    exception leaves the C entry."""
+    script = f"""
+import ctypes, resource, sys
+import torch                     # (what the library's own loading needs, before the limit)
+from fp4_quantized_gemms_b200 import ufp4
+L = ufp4.lib()
+n = 4_000_000
+table = (ufp4.TensorC * n)()
+ctypes.memset(table, 0, ctypes.sizeof(table))
+for i in range(2):
+    table[i] = ufp4.TensorC({P}, {P}, 1, 1, 1)       # twice the same: refused in any case
+args = (table, n, 1.0, {P}, {2 * P}, None)
+size = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (size + (8 << 20),) * 2)
+sys.exit(100 + L.ufp4_grad_clip(*args))
+"""
+    r = subprocess.run([sys.executable, "-c", script], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 100 + UNSUP, (r.returncode, r.stderr[-500:])
